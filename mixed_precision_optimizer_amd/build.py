@@ -24,8 +24,8 @@ ARCH = "gfx950"
 
 
 # gfx950 kernel files and host files of libhpo
-DEVICE_SOURCES = ("hpo_kernels.hip", "hpo_muon.hip", "hpo_static.hip")
-HOST_SOURCES = ("hpo_api.cpp", "hpo_muon_api.cpp")
+DEVICE_SOURCES = ("hpo_kernels.hip", "hpo_muon.hip", "hpo_static.hip", "hpo_rows.hip", "hpo_qk.hip")
+HOST_SOURCES = ("hpo_api.cpp", "hpo_muon_api.cpp", "hpo_stack_api.cpp")
 
 
 def hipcc() -> str:

@@ -57,13 +57,14 @@
 
 #include <type_traits>
 
-#include "hpo_muon_impl.h"
 #include "hpo_device.h"
+#include "hpo_stack_impl.h"
 
 namespace hpo {
 namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
@@ -376,7 +377,33 @@ enum Epi : int {
     kEpiStep = 2,    /* X = bf16(a * X + acc) in place, and X^T    X' = a X + B X */
     kEpiUpdate = 3,  /* O = a * X + acc (fp32) -> master / param update */
     kEpiOut = 4,     /* O = a * X + acc (fp32) -> out, natural layout */
+    /* the stack's iteration: fp16 operands at power-of-two scales (NsStepScale), X as the sum of
+     * an fp16 array and what its rounding lost */
+    kEpiF16Gram = 5, /* C = f16(c * acc) */
+    kEpiF16Poly = 6, /* C = f16(b * P[i][j] + c * acc) */
+    kEpiF16Step = 7, /* x = a * (X + XL 2^-11) + c * acc; X = f16(x) in place, X^T, XL = f16((x - X) 2^11) */
+    kEpiF16Out = 8,  /* bf16(a * X + c * acc) -> out16, natural layout */
 };
+
+/* 2^11: fp16 keeps 11 bits, so what a rounding loses is held again at full precision. */
+constexpr float kLoScale = 2048.0f;
+
+template <bool F16>
+__device__ __forceinline__ f32x16_t ns_mfma(bf16x8_t a, bf16x8_t b, f32x16_t c)
+{
+    if constexpr (F16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
+                                                      0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t f16_bits(float x)
+{
+    return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
+}
+
+__device__ __forceinline__ float f16v(uint16_t b) { return static_cast<float>(__builtin_bit_cast(_Float16, b)); }
 
 struct GemmArgs {
     const uint16_t* P;
@@ -397,6 +424,11 @@ struct GemmArgs {
     float a, b, c;
     int64_t R, Cn;       /* update / out: natural shape; the C tile is in natural orientation */
     float* out;          /* out epilogue */
+    uint16_t* XL;        /* f16 step: what the rounding of X lost (as XS lies; NULL: not kept), read ... */
+    uint16_t* XLn;       /* ... and written, in place (NULL: not wanted by the next step) */
+    int64_t ldxl, sxl;
+    uint16_t* out16;     /* f16 out: bf16 result */
+    int64_t oss, ors;    /* its matrix and row strides */
     const TensorDesc* desc;
     const MuonInfo* info;
     MuonGate gate;
@@ -505,6 +537,7 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
     constexpr int kBM = T::kBM, kBN = T::kBN, kNsThreads = T::kThreads;
     constexpr int kRowStride = T::kRowStride, kPieces = T::kPieces, kRowsPerChunk = T::kRowsPerChunk;
     constexpr int kChunksPerWave = T::kChunksPerWave;
+    constexpr bool kF16 = EPI >= kEpiF16Gram;
     static_assert(!SYM || kBM == kBN, "symmetric outputs mirror square tiles");
     if (!gate_open(g.gate))
         return;
@@ -596,7 +629,7 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
             for (int i = 0; i < kTM; ++i)
 #pragma unroll
                 for (int j = 0; j < kTN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[cur][i], fb[cur][j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = ns_mfma<kF16>(fa[cur][i], fb[cur][j], acc[i][j]);
 #if HPO_NS_SCHED
             if (kk + 1 < kBK / 16) {
                 /* the next slice's kTM + kTN reads spread over this slice's kTM * kTN MFMAs */
@@ -649,7 +682,7 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
             for (int i = 0; i < kTM; ++i)
 #pragma unroll
                 for (int j = 0; j < kTN; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[buf][i], fb[buf][j], acc[i][j], 0, 0, 0);
+                    acc[i][j] = ns_mfma<kF16>(fa[buf][i], fb[buf][j], acc[i][j]);
         };
         auto interleave = [&]() {
             __builtin_amdgcn_sched_barrier(0);   /* one scheduling region per slice */
@@ -851,21 +884,24 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
             }
         };
         const int lcol = lane & 31, lrow4 = 4 * (lane >> 5);
-        auto pack4 = [](float a0, float a1, float a2, float a3) {
+        auto bits16 = [](float x) { return kF16 ? f16_bits(x) : bf16_rne_bits(x); };
+        auto pack4 = [&](float a0, float a1, float a2, float a3) {
             u32x2_t t;
-            t.x = bf16_rne_bits(a0) | (bf16_rne_bits(a1) << 16);
-            t.y = bf16_rne_bits(a2) | (bf16_rne_bits(a3) << 16);
+            t.x = bits16(a0) | (bits16(a1) << 16);
+            t.y = bits16(a2) | (bits16(a3) << 16);
             return t;
         };
         auto unpack = [](u32x2_t t, int e) {
             const uint32_t w = e < 2 ? t.x : t.y;
-            return bf16v(static_cast<uint16_t>(e & 1 ? w >> 16 : w & 0xffffu));
+            const uint16_t b = static_cast<uint16_t>(e & 1 ? w >> 16 : w & 0xffffu);
+            return kF16 ? f16v(b) : bf16v(b);
         };
         __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();   /* every wavefront is past its last fragment read */
-        if constexpr (EPI == kEpiGram || EPI == kEpiPoly) {
+        if constexpr (EPI == kEpiGram || EPI == kEpiPoly || EPI == kEpiF16Gram || EPI == kEpiF16Poly) {
+            constexpr bool kPoly = EPI == kEpiPoly || EPI == kEpiF16Poly;
             const bool diag = SYM && ty == tx;
-            if constexpr (EPI == kEpiPoly) {
+            if constexpr (kPoly) {
                 /* A is symmetric and stored whole: column j of the tile is row col0 + j */
                 stage_in(g.P + z * g.sp + col0 * g.ldp + row0, g.ldp);
                 __syncthreads();
@@ -882,7 +918,12 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
 #pragma clang loop unroll(full)
                         for (int e = 0; e < 4; ++e)
                             x[e] = acc[ti][tj][4 * q + e];
-                        if constexpr (EPI == kEpiPoly) {
+                        if constexpr (EPI == kEpiF16Gram) {
+#pragma clang loop unroll(full)
+                            for (int e = 0; e < 4; ++e)
+                                x[e] = g.c * x[e];
+                        }
+                        if constexpr (kPoly) {
                             const u32x2_t av = *pt;
 #pragma clang loop unroll(full)
                             for (int e = 0; e < 4; ++e) {
@@ -935,6 +976,126 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
             __syncthreads();
             store_n(g.X + z * g.sx + row0 * g.ldx + col0, g.ldx);
             store_t(g.XT + z * g.sxt + col0 * g.ldxt + row0, g.ldxt);
+        } else if constexpr (EPI == kEpiF16Step) {
+            /* acc becomes x; each thread reads and writes the tile's elements it holds */
+            auto each = [&](auto&& f) {
+#pragma clang loop unroll(full)
+                for (int ti = 0; ti < kTM; ++ti)
+#pragma clang loop unroll(full)
+                    for (int tj = 0; tj < kTN; ++tj) {
+#pragma clang loop unroll(full)
+                        for (int q = 0; q < 4; ++q) {
+                            const int i = wm + 32 * ti + 8 * q + lrow4, j = wn + 32 * tj + lcol;
+                            f(acc[ti][tj], 4 * q, reinterpret_cast<u32x2_t*>(Tt + tt(j, i)));
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+            };
+            stage_in(g.XS + z * g.sxs + col0 * g.ldxs + row0, g.ldxs);
+            __syncthreads();
+            each([&](f32x16_t& v, int r, u32x2_t* pt) {
+                const u32x2_t xv = *pt;
+#pragma clang loop unroll(full)
+                for (int e = 0; e < 4; ++e) {
+                    const float ax = g.a * unpack(xv, e), cx = g.c * v[r + e];
+                    v[r + e] = ax + cx;
+                }
+            });
+            if (g.XL != nullptr) {
+                const float al = g.a * (1.0f / kLoScale);
+                __syncthreads();
+                stage_in(g.XL + z * g.sxl + col0 * g.ldxl + row0, g.ldxl);
+                __syncthreads();
+                each([&](f32x16_t& v, int r, u32x2_t* pt) {
+                    const u32x2_t xv = *pt;
+#pragma clang loop unroll(full)
+                    for (int e = 0; e < 4; ++e) {
+                        const float lx = al * unpack(xv, e);
+                        v[r + e] = v[r + e] + lx;
+                    }
+                });
+            }
+            each([&](f32x16_t& v, int r, u32x2_t* pt) { *pt = pack4(v[r], v[r + 1], v[r + 2], v[r + 3]); });
+            __syncthreads();
+            store_n(g.X + z * g.sx + row0 * g.ldx + col0, g.ldx);
+            store_t(g.XT + z * g.sxt + col0 * g.ldxt + row0, g.ldxt);
+            if (g.XLn != nullptr) {
+                __syncthreads();
+                each([&](f32x16_t& v, int r, u32x2_t* pt) {
+                    float l[4];
+#pragma clang loop unroll(full)
+                    for (int e = 0; e < 4; ++e)
+                        l[e] = (v[r + e] - f16v(static_cast<uint16_t>(f16_bits(v[r + e])))) * kLoScale;
+                    *pt = pack4(l[0], l[1], l[2], l[3]);
+                });
+                __syncthreads();
+                store_t(g.XLn + z * g.sxl + col0 * g.ldxl + row0, g.ldxl);
+            }
+        } else if constexpr (EPI == kEpiF16Out) {
+            stage_in(g.XS + z * g.sxs + col0 * g.ldxs + row0, g.ldxs);
+            __syncthreads();
+#pragma clang loop unroll(full)
+            for (int ti = 0; ti < kTM; ++ti)
+#pragma clang loop unroll(full)
+                for (int tj = 0; tj < kTN; ++tj) {
+#pragma clang loop unroll(full)
+                    for (int q = 0; q < 4; ++q) {
+                        const int i = wm + 32 * ti + 8 * q + lrow4, j = wn + 32 * tj + lcol;
+                        u32x2_t* pt = reinterpret_cast<u32x2_t*>(Tt + tt(j, i));
+                        const u32x2_t xv = *pt;
+                        uint32_t b[4];
+#pragma clang loop unroll(full)
+                        for (int e = 0; e < 4; ++e) {
+                            const float ax = g.a * unpack(xv, e), cx = g.c * acc[ti][tj][4 * q + e];
+                            b[e] = bf16_rne_bits(ax + cx);
+                        }
+                        u32x2_t t;
+                        t.x = b[0] | (b[1] << 16);
+                        t.y = b[2] | (b[3] << 16);
+                        *pt = t;
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            __syncthreads();
+            /* 4 rows x 8 columns a block, as store_n, cut to the matrix; whole 16-byte pieces where rows allow */
+            uint16_t* O = g.out16 + z * g.oss;
+            const bool vec = ((reinterpret_cast<uintptr_t>(O) | static_cast<uintptr_t>(2 * g.ors)) & 15) == 0;
+#pragma clang loop unroll(full)
+            for (int k = 0; k < kBlocks; ++k) {
+                const int bidx = tid + k * kNsThreads;
+                const int rest = bidx >> 5;
+                const int par = bidx & 1, jb = ((bidx >> 1) & 15) | ((rest % (kJB / 16)) << 4), ic = rest / (kJB / 16);
+                const int i0 = 8 * ic + 4 * par, j0 = 8 * jb;
+                const int64_t nc = col0 + j0;
+                if (nc >= g.Cn)
+                    continue;
+                u32x2_t v[8];
+#pragma clang loop unroll(full)
+                for (int e = 0; e < 8; ++e)
+                    v[e] = *reinterpret_cast<const u32x2_t*>(Tt + tt(j0 + e, i0));
+#pragma clang loop unroll(full)
+                for (int r = 0; r < 4; ++r) {
+                    const int64_t nr = row0 + i0 + r;
+                    if (nr >= g.R)
+                        break;
+                    const int sh = 16 * (r & 1);
+                    auto el = [&](int e) { return ((r < 2 ? v[e].x : v[e].y) >> sh) & 0xffffu; };
+                    uint16_t* dst = O + nr * g.ors + nc;
+                    if (vec && nc + 8 <= g.Cn) {
+                        u32x4_t o;
+                        o.x = el(0) | (el(1) << 16);
+                        o.y = el(2) | (el(3) << 16);
+                        o.z = el(4) | (el(5) << 16);
+                        o.w = el(6) | (el(7) << 16);
+                        *reinterpret_cast<u32x4_t*>(dst) = o;
+                    } else {
+#pragma clang loop unroll(full)
+                        for (int e = 0; e < 8; ++e)
+                            if (nc + e < g.Cn)
+                                dst[e] = static_cast<uint16_t>(el(e));
+                    }
+                }
+            }
         } else {
             /* last step: O = a X + acc in fp32 (registers), then the master
              * update (or O itself) streamed by rows, half a tile at a time.
@@ -1147,7 +1308,333 @@ hipError_t ns_step(const TensorDesc* d_desc, const MuonInfo* d_info, const MuonB
                   [&] { return launch3(k_ns_gemm<kEpiUpdate, false, GenTile>, grid, GenTile::kThreads, stream, g, up); });
 }
 
+/* ---------------------------------------------------------------------- */
+/* the stack's iteration (hpo_orthogonalize)                               */
+/* ---------------------------------------------------------------------- */
+constexpr int kSumThreads = 512;
+constexpr int64_t kSumMax = 512;      /* partial sums of squares per matrix, at most */
+constexpr int64_t kSumPer = 8192;     /* elements a workgroup sums at the least */
+
+int64_t sum_parts(int64_t rows, int64_t cols)
+{
+    const int64_t p = (rows * cols + kSumPer - 1) / kSumPer;
+    return p < 1 ? 1 : (p > kSumMax ? kSumMax : p);
+}
+
+struct OrthoSrc {
+    const void* G;
+    int64_t gbs, grs;
+    float* M;
+    int64_t mbs, mrs;
+    int64_t rows, cols;
+    MuonScalars sc;
+};
+
+template <bool BF16>
+__device__ __forceinline__ float src_at(const OrthoSrc& s, int64_t off)
+{
+    if constexpr (BF16)
+        return bf16_to_f32(static_cast<const uint16_t*>(s.G)[off]);
+    else
+        return static_cast<const float*>(s.G)[off];
+}
+
+/* g~ of one element from the stored grad and, when there is one, the momentum
+ * after this step's update. */
+__device__ __forceinline__ float nesterov_of(float g, float M, const MuonScalars& sc)
+{
+    if (!sc.nesterov)
+        return M;
+    return sc.form == HPO_MUON_MOMENTUM_SUM ? g + sc.mu * M : sc.omu * g + sc.mu * M;
+}
+
+/* Momentum update in place and the partial sums of g~^2 (grid: parts, batch). */
+template <bool BF16>
+__global__ __launch_bounds__(kSumThreads) void k_stack_momentum(OrthoSrc s, double* part)
+{
+    if (!gate_open(s.sc.gate))
+        return;
+    const GradVals k = grad_vals(s.sc);
+    const int64_t z = blockIdx.y;
+    double acc = 0.0;
+    /* rows are handed out by wavefront: one row at a time, 64 consecutive elements an access */
+    const int64_t wave = static_cast<int64_t>(blockIdx.x) * (kSumThreads / 64) + (threadIdx.x >> 6);
+    const int64_t waves = static_cast<int64_t>(gridDim.x) * (kSumThreads / 64);
+    const int lane = threadIdx.x & 63;
+    /* a wavefront takes a run of 1024 columns of one row */
+    constexpr int64_t kRun = 1024;
+    const int64_t runs = (s.cols + kRun - 1) / kRun;
+    for (int64_t t = wave; t < s.rows * runs; t += waves) {
+        const int64_t i = t / runs, c0 = (t % runs) * kRun;
+        const int64_t c1 = c0 + kRun < s.cols ? c0 + kRun : s.cols;
+        const int64_t g0 = z * s.gbs + i * s.grs, m0 = z * s.mbs + i * s.mrs;
+#pragma unroll 4
+        for (int64_t c = c0 + lane; c < c1; c += 64) {
+            float g = src_at<BF16>(s, g0 + c) * k.inv_scale;
+            if (k.clip)
+                g = g * k.C;
+            float gt = g;
+            if (s.M != nullptr) {
+                float M = s.M[m0 + c];
+                M = s.sc.form == HPO_MUON_MOMENTUM_SUM ? s.sc.mu * M + g : s.sc.mu * M + s.sc.omu * g;
+                s.M[m0 + c] = M;
+                gt = nesterov_of(g, M, s.sc);
+            }
+            acc += static_cast<double>(gt) * static_cast<double>(gt);
+        }
+    }
+    const double tot = block_sum<kSumThreads>(acc);
+    if (threadIdx.x == 0)
+        part[z * gridDim.x + blockIdx.x] = tot;
+}
+
+/* X0 = f16(g~ / (norm + eps) * 2^ex) both ways round, zero-padded, and what the
+ * rounding lost in the X^T orientation (grid: padded columns / 64, rows / 64,
+ * batch; natural orientation, as k_muon_ns_input). */
+template <bool BF16>
+__global__ __launch_bounds__(kBlock) void k_stack_input(OrthoSrc s, const double* part, int32_t parts, float x0_scale,
+                                                        uint16_t* copy, int64_t ld_copy, uint16_t* trans,
+                                                        int64_t ld_trans, int64_t stride, uint16_t* lo,
+                                                        int32_t lo_trans)
+{
+    if (!gate_open(s.sc.gate))
+        return;
+    __shared__ __attribute__((aligned(4))) uint16_t tile[kTile][kTile + 2];
+    __shared__ __attribute__((aligned(4))) uint16_t tlo[kTile][kTile + 2];
+    __shared__ float dnorm;
+    const GradVals k = grad_vals(s.sc);
+    const int64_t z = blockIdx.z;
+    const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kTile;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kTile;
+    const int tid = threadIdx.x;
+    double acc = 0.0;
+    for (int32_t p = tid; p < parts; p += kBlock)
+        acc += part[z * parts + p];
+    const double tot = block_sum<kBlock>(acc);
+    if (tid == 0)
+        dnorm = static_cast<float>(sqrt(tot)) + s.sc.eps;
+    __syncthreads();
+    const float d = dnorm;
+    constexpr int kPer = kTile * kTile / kBlock;
+    float x[kPer];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const int e = tid + q * kBlock;
+        const int64_t gr = r0 + e / kTile, gc = c0 + e % kTile;
+        x[q] = 0.0f;
+        if (gr < s.rows && gc < s.cols) {
+            float g = src_at<BF16>(s, z * s.gbs + gr * s.grs + gc) * k.inv_scale;
+            if (k.clip)
+                g = g * k.C;
+            x[q] = s.M != nullptr ? nesterov_of(g, s.M[z * s.mbs + gr * s.mrs + gc], s.sc) : g;
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+        const int e = tid + q * kBlock;
+        /* 0 / 0 is a matrix of zeros with eps = 0: it stays 0 */
+        const float y = (x[q] == 0.0f ? 0.0f : x[q] / d) * x0_scale;
+        const uint32_t h = f16_bits(y);
+        tile[e / kTile][e % kTile] = static_cast<uint16_t>(h);
+        tlo[e / kTile][e % kTile] = static_cast<uint16_t>(f16_bits((y - f16v(static_cast<uint16_t>(h))) * kLoScale));
+    }
+    __syncthreads();
+    auto row8 = [&](const uint16_t(*t)[kTile + 2], int r, int p) {
+        u32x4_t v;
+        v.x = t[r][p + 0] | (static_cast<uint32_t>(t[r][p + 1]) << 16);
+        v.y = t[r][p + 2] | (static_cast<uint32_t>(t[r][p + 3]) << 16);
+        v.z = t[r][p + 4] | (static_cast<uint32_t>(t[r][p + 5]) << 16);
+        v.w = t[r][p + 6] | (static_cast<uint32_t>(t[r][p + 7]) << 16);
+        return v;
+    };
+    auto col8 = [&](const uint16_t(*t)[kTile + 2], int r, int p) {
+        u32x4_t v;
+        v.x = t[p + 0][r] | (static_cast<uint32_t>(t[p + 1][r]) << 16);
+        v.y = t[p + 2][r] | (static_cast<uint32_t>(t[p + 3][r]) << 16);
+        v.z = t[p + 4][r] | (static_cast<uint32_t>(t[p + 5][r]) << 16);
+        v.w = t[p + 6][r] | (static_cast<uint32_t>(t[p + 7][r]) << 16);
+        return v;
+    };
+#pragma unroll
+    for (int q = 0; q < kTile * kTile / 8 / kBlock; ++q) {
+        const int e = tid + q * kBlock;
+        const int r = e / 8, p = (e % 8) * 8;
+        *reinterpret_cast<u32x4_t*>(copy + z * stride + (r0 + r) * ld_copy + c0 + p) = row8(tile, r, p);
+        *reinterpret_cast<u32x4_t*>(trans + z * stride + (c0 + r) * ld_trans + r0 + p) = col8(tile, r, p);
+        if (lo != nullptr) {
+            if (lo_trans)
+                *reinterpret_cast<u32x4_t*>(lo + z * stride + (c0 + r) * ld_trans + r0 + p) = col8(tlo, r, p);
+            else
+                *reinterpret_cast<u32x4_t*>(lo + z * stride + (r0 + r) * ld_copy + c0 + p) = row8(tlo, r, p);
+        }
+    }
+}
+
+/* Buffers of one slice of a stack. */
+struct OrthoWork {
+    double* part;
+    uint16_t *X, *XT[2], *XL, *A, *B;
+};
+
+struct OrthoPlan {
+    int64_t m, n, mp, np;
+    int64_t parts;
+    int64_t slot;      /* bytes of one matrix */
+    int64_t count;     /* matrices of a slice */
+};
+
+OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols)
+{
+    OrthoPlan p{};
+    p.m = rows > cols ? cols : rows;
+    p.n = rows > cols ? rows : cols;
+    p.mp = ns_pad(p.m);
+    p.np = ns_pad(p.n);
+    p.parts = sum_parts(rows, cols);
+    p.slot = 2 * (4 * p.mp * p.np + 2 * p.mp * p.mp);
+    /* slices of equal size under the cap (one matrix at the least) */
+    constexpr int64_t kCap = int64_t{4} << 30;
+    const int64_t most = kCap / p.slot > 1 ? kCap / p.slot : 1;
+    const int64_t slices = (batch + most - 1) / most;
+    p.count = (batch + slices - 1) / slices;
+    return p;
+}
+
+int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
+
+template <bool BF16>
+hipError_t ortho_slice(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64_t count, hipStream_t stream)
+{
+    const bool tall = a.rows > a.cols;
+    OrthoWork w{};
+    char* at = static_cast<char*>(a.ws);
+    w.part = reinterpret_cast<double*>(at);
+    at += round256(8 * p.count * p.parts);
+    const int64_t xs = p.mp * p.np, as = p.mp * p.mp;
+    auto take = [&](int64_t elems) {
+        uint16_t* r = reinterpret_cast<uint16_t*>(at);
+        at += 2 * elems * p.count;
+        return r;
+    };
+    w.X = take(xs);
+    w.XT[0] = take(xs);
+    w.XT[1] = take(xs);
+    w.XL = take(xs);
+    w.A = take(as);
+    w.B = take(as);
+    OrthoSrc s{};
+    const int64_t esize = BF16 ? 2 : 4;
+    s.G = static_cast<const char*>(a.G.data) + esize * z0 * a.G.bs;
+    s.gbs = a.G.bs;
+    s.grs = a.G.rs;
+    s.M = a.M.data ? static_cast<float*>(a.M.data) + z0 * a.M.bs : nullptr;
+    s.mbs = a.M.bs;
+    s.mrs = a.M.rs;
+    s.rows = a.rows;
+    s.cols = a.cols;
+    s.sc = a.sc;
+    const uint32_t cnt = static_cast<uint32_t>(count);
+    hipError_t e = launch3(k_stack_momentum<BF16>, dim3(static_cast<uint32_t>(p.parts), cnt), kSumThreads, stream, s,
+                           w.part);
+    if (e != hipSuccess)
+        return e;
+    const int64_t Rp = tall ? p.np : p.mp, Cp = tall ? p.mp : p.np;
+    /* what the rounding of X loses is worth keeping for every step that another one follows */
+    const bool lo0 = a.steps > 1;
+    e = launch3(k_stack_input<BF16>,
+                dim3(static_cast<uint32_t>(Cp / kTile), static_cast<uint32_t>(Rp / kTile), cnt), kBlock, stream, s,
+                static_cast<const double*>(w.part), static_cast<int32_t>(p.parts), a.x0_scale, tall ? w.XT[0] : w.X,
+                tall ? p.mp : p.np, tall ? w.X : w.XT[0], tall ? p.np : p.mp, xs, lo0 ? w.XL : nullptr,
+                static_cast<int32_t>(tall ? 0 : 1));
+    if (e != hipSuccess)
+        return e;
+    const MuonUpdate up{};
+    int cur = 0;
+    for (int32_t k = 0; k < a.steps; ++k) {
+        const bool last = k + 1 == a.steps;
+        const NsStepScale& f = a.step[k];
+        GemmArgs g{};
+        g.gate = a.sc.gate;
+        g.P = w.X; g.ldp = p.np; g.sp = xs;
+        g.Q = w.X; g.ldq = p.np; g.sq = xs;
+        g.K = static_cast<int32_t>(p.np);
+        g.C = w.A; g.ldc = p.mp; g.sc = as;
+        g.c = f.gram;
+        g.nt = static_cast<int32_t>(p.mp / SymTile::kBM);
+        const dim3 tri(static_cast<uint32_t>(g.nt * (g.nt + 1) / 2), 1, cnt);
+        e = launch3(k_ns_gemm<kEpiF16Gram, true, SymTile>, tri, SymTile::kThreads, stream, g, up);
+        if (e != hipSuccess)
+            return e;
+        g.P = w.A; g.ldp = p.mp; g.sp = as;
+        g.Q = w.A; g.ldq = p.mp; g.sq = as;
+        g.K = static_cast<int32_t>(p.mp);
+        g.C = w.B;
+        g.b = f.poly_b;
+        g.c = f.poly_c;
+        e = launch3(k_ns_gemm<kEpiF16Poly, true, SymTile>, tri, SymTile::kThreads, stream, g, up);
+        if (e != hipSuccess)
+            return e;
+        g.P = w.B; g.ldp = p.mp; g.sp = as;
+        g.Q = w.XT[cur]; g.ldq = p.mp; g.sq = xs;
+        g.X = w.X; g.ldx = p.np; g.sx = xs;
+        g.XT = w.XT[cur ^ 1]; g.ldxt = p.mp; g.sxt = xs;
+        g.XS = w.XT[cur]; g.ldxs = p.mp; g.sxs = xs;
+        g.ldxl = p.mp;
+        g.sxl = xs;
+        g.a = f.step_a;
+        g.c = f.step_c;
+        g.nx = static_cast<int32_t>(p.np / GenTile::kBN);
+        g.ny = static_cast<int32_t>(p.mp / GenTile::kBM);
+        if (!last) {
+            g.XL = w.XL;
+            g.XLn = k + 2 < a.steps ? w.XL : nullptr;
+            e = launch3(k_ns_gemm<kEpiF16Step, false, GenTile>, dim3(static_cast<uint32_t>(g.nx * g.ny), 1, cnt),
+                        GenTile::kThreads, stream, g, up);
+        } else {
+            g.R = p.m;
+            g.Cn = p.n;
+            if (tall) {   /* O^T = a X^T + X^T B: the tile comes out in the output's own order */
+                g.P = w.XT[cur]; g.ldp = p.mp; g.sp = xs;
+                g.Q = w.B; g.ldq = p.mp; g.sq = as;
+                g.XS = w.X; g.ldxs = p.np; g.sxs = xs;
+                g.nx = static_cast<int32_t>(p.mp / GenTile::kBN);
+                g.ny = static_cast<int32_t>(p.np / GenTile::kBM);
+                g.R = p.n;
+                g.Cn = p.m;
+            }
+            g.out16 = static_cast<uint16_t*>(a.out.data) + z0 * a.out.bs;
+            g.oss = a.out.bs;
+            g.ors = a.out.rs;
+            e = launch3(k_ns_gemm<kEpiF16Out, false, GenTile>, dim3(static_cast<uint32_t>(g.nx * g.ny), 1, cnt),
+                        GenTile::kThreads, stream, g, up);
+        }
+        if (e != hipSuccess)
+            return e;
+        cur ^= 1;
+    }
+    return hipSuccess;
+}
+
 }  // namespace
+
+int64_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols)
+{
+    const OrthoPlan p = ortho_plan(batch, rows, cols);
+    return round256(8 * p.count * p.parts) + p.count * p.slot;
+}
+
+hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t stream)
+{
+    const OrthoPlan p = ortho_plan(a.batch, a.rows, a.cols);
+    for (int64_t z = 0; z < a.batch; z += p.count) {
+        const int64_t count = a.batch - z < p.count ? a.batch - z : p.count;
+        const hipError_t e = a.g_bf16 ? ortho_slice<true>(a, p, z, count, stream)
+                                      : ortho_slice<false>(a, p, z, count, stream);
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
 
 hipError_t launch_muon_momentum(const SetView& sv, const MuonInfo* d_info, const MuonBatch& b, const MuonScalars& sc,
                                 const MuonWork& w, hipStream_t stream)

@@ -82,33 +82,6 @@ void ns_coeffs(const hpo_muon_cfg* cfg, float* out)
     }
 }
 
-hpo_status check_muon_cfg(const hpo_muon_cfg* cfg, bool ns_only)
-{
-    if (!cfg)
-        return fail(HPO_EINVAL, "cfg is NULL");
-    if (cfg->ns_steps < 1 || cfg->ns_steps > HPO_NS_MAX_STEPS)
-        return fail(HPO_EINVAL, "ns_steps must be in [1, %d] (got %d)", HPO_NS_MAX_STEPS, cfg->ns_steps);
-    if (!(cfg->ns_eps >= 0.0) || !is_finite(cfg->ns_eps))
-        return fail(HPO_EINVAL, "ns_eps must be finite and >= 0 (got %g)", cfg->ns_eps);
-    if (cfg->ns_coeffs)
-        for (int32_t k = 0; k < 3 * cfg->ns_steps; ++k)
-            if (!is_finite(cfg->ns_coeffs[k]))
-                return fail(HPO_EINVAL, "ns_coeffs[%d] is not finite", k);
-    if (ns_only)
-        return HPO_OK;
-    if (!(cfg->momentum >= 0.0 && cfg->momentum < 1.0))
-        return fail(HPO_EINVAL, "momentum must lie in [0, 1) (got %g)", cfg->momentum);
-    if (cfg->nesterov != 0 && cfg->nesterov != 1)
-        return fail(HPO_EINVAL, "nesterov must be 0 or 1 (got %d)", cfg->nesterov);
-    if (cfg->momentum_form != HPO_MUON_MOMENTUM_SUM && cfg->momentum_form != HPO_MUON_MOMENTUM_EMA)
-        return fail(HPO_EINVAL, "momentum_form %d is not a hpo_muon_momentum", cfg->momentum_form);
-    if (cfg->scale_mode < HPO_MUON_SCALE_SPECTRAL || cfg->scale_mode > HPO_MUON_SCALE_UNIT_RMS)
-        return fail(HPO_EINVAL, "scale_mode %d is not a hpo_muon_scale", cfg->scale_mode);
-    if (!(cfg->extra_scale >= 0.0) || !is_finite(cfg->extra_scale))
-        return fail(HPO_EINVAL, "extra_scale must be finite and >= 0 (got %g)", cfg->extra_scale);
-    return HPO_OK;
-}
-
 /* Records one event of the profile pool on `stream`; returns its index. */
 size_t prof_mark(hpo_muon_prof& p, hipStream_t stream)
 {
@@ -154,6 +127,33 @@ void free_prof(hpo_muon_prof* p)
 }  // namespace
 
 namespace hpo_host {
+
+hpo_status check_muon_cfg(const hpo_muon_cfg* cfg, bool ns_only)
+{
+    if (!cfg)
+        return fail(HPO_EINVAL, "cfg is NULL");
+    if (cfg->ns_steps < 1 || cfg->ns_steps > HPO_NS_MAX_STEPS)
+        return fail(HPO_EINVAL, "ns_steps must be in [1, %d] (got %d)", HPO_NS_MAX_STEPS, cfg->ns_steps);
+    if (!(cfg->ns_eps >= 0.0) || !is_finite(cfg->ns_eps))
+        return fail(HPO_EINVAL, "ns_eps must be finite and >= 0 (got %g)", cfg->ns_eps);
+    if (cfg->ns_coeffs)
+        for (int32_t k = 0; k < 3 * cfg->ns_steps; ++k)
+            if (!is_finite(cfg->ns_coeffs[k]))
+                return fail(HPO_EINVAL, "ns_coeffs[%d] is not finite", k);
+    if (ns_only)
+        return HPO_OK;
+    if (!(cfg->momentum >= 0.0 && cfg->momentum < 1.0))
+        return fail(HPO_EINVAL, "momentum must lie in [0, 1) (got %g)", cfg->momentum);
+    if (cfg->nesterov != 0 && cfg->nesterov != 1)
+        return fail(HPO_EINVAL, "nesterov must be 0 or 1 (got %d)", cfg->nesterov);
+    if (cfg->momentum_form != HPO_MUON_MOMENTUM_SUM && cfg->momentum_form != HPO_MUON_MOMENTUM_EMA)
+        return fail(HPO_EINVAL, "momentum_form %d is not a hpo_muon_momentum", cfg->momentum_form);
+    if (cfg->scale_mode < HPO_MUON_SCALE_SPECTRAL || cfg->scale_mode > HPO_MUON_SCALE_UNIT_RMS)
+        return fail(HPO_EINVAL, "scale_mode %d is not a hpo_muon_scale", cfg->scale_mode);
+    if (!(cfg->extra_scale >= 0.0) || !is_finite(cfg->extra_scale))
+        return fail(HPO_EINVAL, "extra_scale must be finite and >= 0 (got %g)", cfg->extra_scale);
+    return HPO_OK;
+}
 
 void free_muon(hpo_muon_part* m)
 {

@@ -1,0 +1,376 @@
+/*
+ * hpo_qk.hip -- gfx950 kernels of hpo_qk_max_logits: the largest attention
+ * logit of each head, S_h = max over the seen pairs of scale * (q . k).
+ *
+ * Source: [OPT-INFRA] "02 · Optimizer：算法与 infra" (llm-infra-atlas,
+ * train/02_optimizer), §6: the S_max^h that QK-clip compares with its threshold.
+ *
+ * The logits are a matrix product of which only the maximum leaves the chip,
+ * so the work is bound by the matrix cores.  A workgroup of four wavefronts
+ * takes 256 queries of one head (64 per wavefront, their fragments in
+ * registers for the whole pass) against key tiles of 64, staged in LDS in two
+ * buffers; a key tile is the MFMA's row operand, so a lane's 16 results of one
+ * 32 x 32 block are keys of one query, and its limits (causal, window,
+ * lengths) are two numbers.  Tiles that every query of the wavefront sees whole skip
+ * the mask, tiles none sees skip the products.  The maximum needs no state per query:
+ * each lane keeps one number, folded with v_maximum3 (two logits an
+ * instruction, NaN stays NaN).
+ */
+#include <hip/hip_runtime.h>
+
+#include <type_traits>
+
+#include "hpo_device.h"
+#include "hpo_stack_impl.h"
+
+namespace hpo {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kQkThreads = 256;
+constexpr int kQkWaves = 4;
+constexpr int kWaveRows = 64;                      /* queries of a wavefront */
+constexpr int kTileQ = kWaveRows * kQkWaves;       /* queries of a workgroup */
+constexpr int kTileK = 64;                         /* keys of a stage */
+
+template <bool FP16>
+__device__ __forceinline__ f32x16_t mfma(u32x4_t a, u32x4_t b, f32x16_t c)
+{
+    if constexpr (FP16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c,
+                                                      0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                       __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+/* Byte offset of 16-byte piece p of LDS row r (rows of DP elements).  The
+ * pieces of a row are permuted by an XOR of the row, so that the 16 rows a
+ * fragment read serves at a time lie in distinct banks. */
+template <int DP>
+__device__ __forceinline__ int swizzle(int r)
+{
+    if constexpr (DP % 128 == 0)
+        return r & 15;
+    else
+        return (r & 7) ^ ((r >> 3) & 1);
+}
+
+template <int DP>
+__device__ __forceinline__ int piece_at(int r, int p)
+{
+    return r * (DP * 2) + ((p ^ swizzle<DP>(r)) << 4);
+}
+
+/* 64 x 16 bytes from a buffer straight into LDS: lane l's lands at dst + 16 l. */
+__device__ __forceinline__ void buffer_load_lds16(__amdgpu_buffer_rsrc_t rs, char* dst, int voff)
+{
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, voff, 0, 0, 0);
+}
+
+/* Eight elements of a row of `dim`, from element d on; 0 behind its end. */
+__device__ __forceinline__ u32x4_t load8(const uint16_t* row, int d, int dim, bool aligned)
+{
+    u32x4_t v = {0, 0, 0, 0};
+    if (aligned && d + 8 <= dim)
+        return *reinterpret_cast<const u32x4_t*>(row + d);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (d + e < dim)
+            v[e >> 1] |= static_cast<uint32_t>(row[d + e]) << (16 * (e & 1));
+    return v;
+}
+
+__device__ __forceinline__ float maximum(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+/* Work of one workgroup in dispatch order.  Workgroups go to the 8 XCDs
+ * round-robin: each XCD gets one contiguous run, so the heads and query tiles
+ * that read one key head meet in its L2. */
+__device__ __forceinline__ int64_t xcd_run(int64_t b, int64_t n)
+{
+    constexpr int64_t kXcd = 8;
+    const int64_t x = b % kXcd, k = b / kXcd, q = n / kXcd, r = n % kXcd;
+    return (x < r ? x * (q + 1) : r * (q + 1) + (x - r) * q) + k;
+}
+
+/* One sequence: its first token and its length, cut to what is there. */
+__device__ __forceinline__ void extent(const int32_t* cu, const int32_t* len, int b, int seq, int& start, int& n)
+{
+    start = 0;
+    n = seq;
+    if (cu != nullptr) {
+        const int lo = cu[b], hi = cu[b + 1];
+        start = lo < 0 ? 0 : (lo > seq ? seq : lo);
+        const int end = hi < start ? start : (hi > seq ? seq : hi);
+        n = end - start;
+    } else if (len != nullptr) {
+        const int l = len[b];
+        n = l < 0 ? 0 : (l > seq ? seq : l);
+    }
+}
+
+/* DIRECT: dim == DP and every row 16-byte aligned, key tiles go straight from
+ * global memory into LDS; else they pass through registers, zero-filled to DP. */
+template <bool FP16, int DP, bool DIRECT>
+__global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a, int aligned)
+{
+    constexpr int kSlices = DP / 16;
+    constexpr int kPieces = DP / 8;
+    constexpr int kStageBytes = kTileK * DP * 2;
+    constexpr int kChunks = kStageBytes / 1024 / kQkWaves;   /* 1 KB loads of a wavefront per stage */
+    __shared__ __attribute__((aligned(16))) char lds[2 * kStageBytes];
+    __shared__ float wmax[kQkWaves];
+    const int tid = threadIdx.x;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int per = a.heads / a.kv_heads;
+    int64_t t = xcd_run(blockIdx.x, gridDim.x);
+    const int split = static_cast<int>(t % a.splits);
+    t /= a.splits;
+    const int hg = static_cast<int>(t % per);
+    t /= per;
+    const int tile0 = a.q_tiles - 1 - static_cast<int>(t % a.q_tiles);   /* the longest causal rows first */
+    t /= a.q_tiles;
+    const int hk = static_cast<int>(t % a.kv_heads), b = static_cast<int>(t / a.kv_heads);
+    const int h = hk * per + hg;
+    int q_start, len_q, k_start, len_k;
+    extent(a.cu_q, a.len_q, b, a.seq_q, q_start, len_q);
+    extent(a.cu_k, a.len_k, b, a.seq_k, k_start, len_k);
+    if (len_q == 0 || len_k == 0)
+        return;
+    const int off = len_k - len_q;
+    const uint16_t* __restrict__ Q = a.q + (a.cu_q ? 0 : b * a.qsb) + q_start * a.qst + h * a.qsh;
+    const uint16_t* __restrict__ K = a.k + (a.cu_k ? 0 : b * a.ksb) + k_start * a.kst + hk * a.ksh;
+    const int nks = DIRECT ? kSlices : (a.dim + 15) / 16;   /* slices that are not all padding */
+    const int frow = lane & 31, fhalf = lane >> 5;
+    float best = -INFINITY;
+
+    for (int qt = tile0; static_cast<int64_t>(qt) * kTileQ < len_q; qt += a.q_tiles) {
+        const int q0 = qt * kTileQ;
+        const int q1 = q0 + kTileQ < len_q ? q0 + kTileQ : len_q;
+        /* keys that some query of the tile sees */
+        int lo = 0, hi = len_k - 1;
+        if (a.causal) {
+            hi = q1 - 1 + off < hi ? q1 - 1 + off : hi;
+            if (a.window >= 0 && q0 + off - a.window > 0)
+                lo = q0 + off - a.window;
+        }
+        if (hi < lo)
+            continue;
+        const int first = lo / kTileK, count = hi / kTileK - first + 1;
+        const int t0 = first + static_cast<int>(static_cast<int64_t>(count) * split / a.splits);
+        const int t1 = first + static_cast<int>(static_cast<int64_t>(count) * (split + 1) / a.splits);
+        if (t0 >= t1)
+            continue;
+
+        /* this wavefront's queries: fragments and each lane's key limits */
+        const int w0 = q0 + wave * kWaveRows;
+        u32x4_t fq[2][kSlices];
+        int klo[2], khi[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int i = w0 + 32 * j + frow;
+            const uint16_t* row = Q + static_cast<int64_t>(i < len_q ? i : len_q - 1) * a.qst;
+#pragma unroll
+            for (int s = 0; s < kSlices; ++s) {
+                if constexpr (DIRECT)
+                    fq[j][s] = *reinterpret_cast<const u32x4_t*>(row + 16 * s + 8 * fhalf);
+                else
+                    fq[j][s] = load8(row, 16 * s + 8 * fhalf, a.dim, aligned);
+            }
+            khi[j] = len_k - 1;
+            klo[j] = 0;
+            if (a.causal) {
+                khi[j] = i + off < khi[j] ? i + off : khi[j];
+                if (a.window >= 0 && i + off - a.window > 0)
+                    klo[j] = i + off - a.window;
+            }
+            if (i >= len_q)
+                khi[j] = -1;
+        }
+        /* the wavefront's limits: seen by some query, seen by every query */
+        const int wlast = w0 + kWaveRows - 1 < len_q ? w0 + kWaveRows - 1 : len_q - 1;
+        int some_hi = w0 < len_q ? len_k - 1 : -1, every_hi = w0 + kWaveRows <= len_q ? len_k - 1 : -1;
+        int some_lo = 0, every_lo = 0;
+        if (a.causal) {
+            some_hi = wlast + off < some_hi ? wlast + off : some_hi;
+            every_hi = w0 + off < every_hi ? w0 + off : every_hi;
+            if (a.window >= 0) {
+                some_lo = w0 + off - a.window > 0 ? w0 + off - a.window : 0;
+                every_lo = wlast + off - a.window > 0 ? wlast + off - a.window : 0;
+            }
+        }
+
+        auto stage = [&](int kt, int buf) {
+            const int k0 = kt * kTileK;
+            const int left = len_k - k0;   /* >= 1 */
+            const uint16_t* base = K + static_cast<int64_t>(k0) * a.kst;
+            char* dst = lds + buf * kStageBytes;
+            if constexpr (DIRECT) {
+                /* rows behind the end repeat the last one: in bounds, and masked */
+                const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+                    const_cast<uint16_t*>(base), 0, 0x7fffffff, 0x00020000);
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const int at = (wave * kChunks + c) * 64 + lane;
+                    const int r = at / kPieces, p = (at % kPieces) ^ swizzle<DP>(r);
+                    const int rr = r < left ? r : left - 1;
+                    buffer_load_lds16(rs, dst + (wave * kChunks + c) * 1024,
+                                      (rr * static_cast<int>(a.kst) + p * 8) * 2);
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < kChunks; ++c) {
+                    const int at = c * kQkThreads + tid;
+                    const int r = at / kPieces, p = at % kPieces;
+                    const int rr = r < left ? r : left - 1;
+                    const u32x4_t v = load8(base + static_cast<int64_t>(rr) * a.kst, p * 8, a.dim, aligned);
+                    *reinterpret_cast<u32x4_t*>(dst + piece_at<DP>(r, p)) = v;
+                }
+            }
+        };
+
+        auto compute = [&](int kt, int buf) {
+            const int k0 = kt * kTileK;
+            if (k0 > some_hi || k0 + kTileK - 1 < some_lo)
+                return;
+            const char* src = lds + buf * kStageBytes;
+            f32x16_t acc[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[i][j] = f32x16_t{};
+#pragma unroll
+            for (int s = 0; s < kSlices; ++s) {
+                if (DIRECT || s < nks) {
+                    u32x4_t fk[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        fk[i] = *reinterpret_cast<const u32x4_t*>(src + piece_at<DP>(32 * i + frow, 2 * s + fhalf));
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            acc[i][j] = mfma<FP16>(fk[i], fq[j][s], acc[i][j]);
+                }
+            }
+            if (k0 >= every_lo && k0 + kTileK - 1 <= every_hi) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            best = maximum(best, acc[i][j][r]);
+            } else {
+                /* acc[i][j][r]: key k0 + 32 i + 8 (r / 4) + 4 (lane / 32) + r % 4, query of this lane */
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) {
+                            const int key = k0 + 32 * i + 8 * (r >> 2) + 4 * fhalf + (r & 3);
+                            best = maximum(best, key >= klo[j] && key <= khi[j] ? acc[i][j][r] : -INFINITY);
+                        }
+            }
+        };
+
+        /* one barrier per stage: behind it every wavefront's part of stage kt is in LDS, and the
+         * other buffer is no longer read */
+        __syncthreads();   /* the buffers of the previous query tile */
+        stage(t0, 0);
+        for (int kt = t0; kt < t1; ++kt) {
+            const int buf = (kt - t0) & 1;
+            __syncthreads();
+            if (kt + 1 < t1)
+                stage(kt + 1, buf ^ 1);
+            compute(kt, buf);
+        }
+    }
+
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1)
+        best = maximum(best, __shfl_xor(best, d, 64));
+    if (lane == 0)
+        wmax[wave] = best;
+    __syncthreads();
+    if (tid == 0) {
+        best = maximum(maximum(wmax[0], wmax[1]), maximum(wmax[2], wmax[3]));
+        /* rounding is monotone: the largest product times scale is the largest logit.  Adding 0
+         * turns -0 into 0.  As bits, non-negative values (and the positive NaN above
+         * them) order as signed integers, negative ones fall as unsigned grow; each atomic
+         * only ever raises the value, so their order does not matter. */
+        const float v = best * a.scale + 0.0f;
+        float* out = a.out + h;
+        if (v != v)
+            atomicMax(reinterpret_cast<int*>(out), 0x7fc00000);
+        else if (v >= 0.0f)
+            atomicMax(reinterpret_cast<int*>(out), __float_as_int(v));
+        else if (v > -INFINITY)
+            atomicMin(reinterpret_cast<unsigned int*>(out), __float_as_uint(v));
+    }
+}
+
+__global__ void k_fill(float* out, int n, float v)
+{
+    const int i = blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < n)
+        out[i] = v;
+}
+
+template <typename... Args>
+hipError_t launch(void (*kernel)(Args...), dim3 grid, int block, hipStream_t stream, Args... args)
+{
+    void* argv[] = {static_cast<void*>(&args)...};
+    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(block), argv, 0, stream);
+}
+
+template <bool FP16, int DP>
+hipError_t launch_dim(const QkArgs& a, bool aligned, uint32_t grid, hipStream_t stream)
+{
+    if (aligned && a.dim == DP)
+        return launch(k_qk_max<FP16, DP, true>, dim3(grid), kQkThreads, stream, a, 1);
+    return launch(k_qk_max<FP16, DP, false>, dim3(grid), kQkThreads, stream, a, aligned ? 1 : 0);
+}
+
+template <bool FP16>
+hipError_t launch_type(const QkArgs& a, bool aligned, uint32_t grid, hipStream_t stream)
+{
+    if (a.dim <= 64)
+        return launch_dim<FP16, 64>(a, aligned, grid, stream);
+    if (a.dim <= 128)
+        return launch_dim<FP16, 128>(a, aligned, grid, stream);
+    if (a.dim <= 192)
+        return launch_dim<FP16, 192>(a, aligned, grid, stream);
+    return launch_dim<FP16, 256>(a, aligned, grid, stream);
+}
+
+}  // namespace
+
+hipError_t launch_qk_max(QkArgs a, bool fp16, bool aligned, bool accumulate, hipStream_t stream)
+{
+    if (!accumulate) {
+        hipError_t e = launch(k_fill, dim3((a.heads + 255) / 256), 256, stream, a.out, static_cast<int>(a.heads), -INFINITY);
+        if (e != hipSuccess)
+            return e;
+    }
+    if (a.batch == 0 || a.seq_q == 0 || a.seq_k == 0)
+        return hipSuccess;
+    a.q_tiles = (a.max_q + kTileQ - 1) / kTileQ;
+    const int64_t tiles = static_cast<int64_t>(a.batch) * a.heads * a.q_tiles;
+    /* Few query tiles: the keys are split until the chip's 512 resident workgroups have work, with
+     * four stages each at the least. */
+    const int64_t want = (512 + tiles - 1) / tiles, most = (a.max_k + 4 * kTileK - 1) / (4 * kTileK);
+    a.splits = static_cast<int32_t>(want < most ? want : most);
+    if (a.splits < 1)
+        a.splits = 1;
+    const uint32_t grid = static_cast<uint32_t>(tiles * a.splits);
+    return fp16 ? launch_type<true>(a, aligned, grid, stream) : launch_type<false>(a, aligned, grid, stream);
+}
+
+}  // namespace hpo

@@ -113,6 +113,8 @@ hpo::Partials partials_of(hpo_set s);
 
 /* hpo_muon_api.cpp */
 void free_muon(hpo_muon_part* m);
+/* Validates a Muon configuration (ns_only: just what Newton-Schulz reads). */
+hpo_status check_muon_cfg(const hpo_muon_cfg* cfg, bool ns_only);
 /* Validates a Muon configuration and the groups against a Muon set. */
 hpo_status check_muon_step(hpo_set s, const hpo_muon_cfg* cfg, const hpo_group* groups, int32_t n_groups,
                            double max_norm);
