@@ -1,0 +1,807 @@
+/*
+ * hpo_gram.hip -- gfx950 kernels of hpo_orthogonalize for matrices whose short
+ * side m is at most 128 (the heads of a projection, thin or tiny matrices).
+ *
+ * Every step of Newton-Schulz multiplies X from the left by a polynomial of
+ * A = X X^T, so with S = X0 X0^T all of them act in the m x m space:
+ *     A_0 = S;   Q_k = a I + b A_k + c A_k^2;   A_{k+1} = Q_k A_k Q_k;
+ *     O = (Q_last ... Q_1 Q_0) X0 = P X0
+ * and the long side n is touched twice (S, then P X0) instead of twice a step.
+ *   gram     one pass over the gradient (and the momentum, updated in place):
+ *            partial S of a run of columns on the matrix cores
+ *   iterate  one workgroup per matrix: S, its trace (the norm), the steps in LDS
+ *   apply    O = P X0 in a second pass
+ * P grows to a^steps in the directions of the small singular values, so every
+ * product carries 22 bits: x = h + l with h = f16(x), l = f16(x - h) at a
+ * power-of-two scale, and x y = h h + h l + l h (the dropped l l is 2^-22 of it) with
+ * fp32 sums.  In the Gram product the two mixed terms are transposes of each other:
+ * h (h + 2 l)^T, made symmetric afterwards, is the same sum in two products.
+ * The scale of the raw gradient is not known before the norm is: a workgroup
+ * keeps a running exponent of its largest magnitude and, when it grows, scales its
+ * sums down (an exact power of two), as an online softmax does with its maximum.
+ *
+ * Source: [HANDBOOK] "优化器：AdamW、Muon 与分布式优化器" (ai-infra-handbooks,
+ * train/algo/optimizer), section on Muon: the iteration and its coefficients.
+ *
+ * Floating point: built with -ffp-contract=off; every elementwise operation
+ * rounds on its own, in the order written.
+ */
+#include <hip/hip_runtime.h>
+
+#include "hpo_muon_device.h"
+
+namespace hpo {
+namespace {
+
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+
+constexpr int kThreads = 256;
+constexpr int kTileElems = 8192;   /* elements of a column tile: 32 per thread */
+constexpr int kTop = 14;           /* values are scaled to at most 2^14 */
+
+struct GramArgs {
+    OrthoSrc s;
+    int64_t m, n;        /* short and long side */
+    int64_t run;         /* columns (of the wide form) a workgroup takes, whole tiles */
+    int32_t chunks;      /* workgroups per matrix */
+    int32_t g_vec;       /* rows of G, M and out take 4-element accesses */
+    int32_t m_vec;
+    int32_t o_vec;
+    float* part;         /* [batch][chunks][MP][MP] */
+    int32_t* part_exp;   /* [batch][chunks] */
+    uint16_t* P;         /* [batch][2][MP][MP]: h and l of P * 2^p_exp */
+    float* inv;          /* [batch][2]: 2^-14 d as (mantissa of 1 / d, exponent) */
+    uint16_t* out;
+    int64_t obs, ors;
+    int32_t steps;
+    int32_t p_exp;       /* exponent of the final P */
+    GramStep step[HPO_NS_MAX_STEPS];
+};
+
+__device__ __forceinline__ f32x16_t mfma(u32x4_t a, u32x4_t b, f32x16_t c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0,
+                                                  0, 0);
+}
+
+/* Byte offset of 16-byte piece p of an LDS row of ROW elements, the pieces
+ * permuted by the row so that a fragment's 16 rows meet distinct banks. */
+template <int ROW>
+__device__ __forceinline__ int piece_at(int r, int p)
+{
+    int f;
+    if constexpr (ROW >= 128)
+        f = r & 15;
+    else if constexpr (ROW == 64)
+        f = (r & 7) ^ ((r >> 3) & 1);
+    else
+        f = (r ^ (r >> 2)) & 3;
+    return r * (ROW * 2) + ((p ^ f) << 4);
+}
+
+template <int ROW>
+__device__ __forceinline__ u32x4_t fragment(const char* base, int row0, int slice)
+{
+    const int lane = threadIdx.x & 63;
+    return *reinterpret_cast<const u32x4_t*>(base + piece_at<ROW>(row0 + (lane & 31), 2 * slice + (lane >> 5)));
+}
+
+/* Four consecutive stored elements: n of them are there (the others read as 0). */
+template <bool BF16>
+__device__ __forceinline__ f32x4_t grad4(const OrthoSrc& s, int64_t at, int n, bool vec)
+{
+    f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (vec && n >= 4) {
+        if constexpr (BF16) {
+            const u32x2_t t = *reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(s.G) + at);
+            x[0] = bf16_to_f32(t.x & 0xffffu);
+            x[1] = bf16_to_f32(t.x >> 16);
+            x[2] = bf16_to_f32(t.y & 0xffffu);
+            x[3] = bf16_to_f32(t.y >> 16);
+        } else {
+            x = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(s.G) + at);
+        }
+        return x;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < n)
+            x[e] = src_at<BF16>(s, at + e);
+    return x;
+}
+
+__device__ __forceinline__ f32x4_t momentum4(const OrthoSrc& s, int64_t at, int n, bool vec)
+{
+    f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (vec && n >= 4)
+        return *reinterpret_cast<const f32x4_t*>(s.M + at);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < n)
+            x[e] = s.M[at + e];
+    return x;
+}
+
+/* A thread's share of one column tile, as eight runs of four elements that lie
+ * together in memory.  ALONG: the eight consecutive elements of an LDS piece run
+ * along memory (two runs a piece, four pieces); else across it (eight memory rows,
+ * four pieces side by side).
+ * LROW x LCOL is the LDS tile (LCOL consecutive elements per row). */
+template <int LROW, int LCOL, bool ALONG>
+struct Share {
+    /* LDS row and first LDS column of piece q (0..3) */
+    __device__ static __forceinline__ void piece(int q, int& r, int& c)
+    {
+        const int t = threadIdx.x;
+        if constexpr (ALONG) {
+            const int p = t + q * kThreads;
+            r = p / (LCOL / 8);
+            c = (p % (LCOL / 8)) * 8;
+        } else {
+            r = (t % (LROW / 4)) * 4 + q;
+            c = (t / (LROW / 4)) * 8;
+        }
+    }
+    /* run j (0..7): its LDS coordinates (first element) */
+    __device__ static __forceinline__ void run(int j, int& r, int& c)
+    {
+        if constexpr (ALONG) {
+            piece(j >> 1, r, c);
+            c += 4 * (j & 1);
+        } else {
+            piece(0, r, c);
+            c += j;
+        }
+    }
+    /* element e (0..7) of piece q among the runs' values */
+    __device__ static __forceinline__ float at(const f32x4_t (&v)[8], int q, int e)
+    {
+        return ALONG ? v[2 * q + (e >> 2)][e & 3] : v[e][q];
+    }
+};
+
+/* g~ of a share.  LDS row = short side (GRAM) or long side (apply); UPDATE
+ * writes the momentum, else it is read as it is after the update. */
+template <bool BF16, bool TALL, bool GRAM, int LROW, int LCOL>
+__device__ __forceinline__ void load_share(const GramArgs& a, const GradVals& k, int64_t z, int64_t k0, f32x4_t (&v)[8])
+{
+    constexpr bool kAlong = GRAM != TALL;   /* LDS columns run along memory */
+    using Sh = Share<LROW, LCOL, kAlong>;
+    const OrthoSrc& s = a.s;
+    f32x4_t mom[8];
+    int64_t row[8], col[8];
+    int cnt[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        int r, c;
+        Sh::run(j, r, c);
+        const int64_t i = GRAM ? r : c, kk = k0 + (GRAM ? c : r);   /* short, long coordinate */
+        row[j] = TALL ? kk : i;
+        col[j] = TALL ? i : kk;
+        const int64_t left = row[j] < s.rows ? s.cols - col[j] : 0;
+        cnt[j] = left >= 4 ? 4 : (left > 0 ? static_cast<int>(left) : 0);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        v[j] = grad4<BF16>(s, z * s.gbs + row[j] * s.grs + col[j], cnt[j], a.g_vec);
+    if (s.M != nullptr) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            mom[j] = momentum4(s, z * s.mbs + row[j] * s.mrs + col[j], cnt[j], a.m_vec);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float g = v[j][e] * k.inv_scale;
+            if (k.clip)
+                g = g * k.C;
+            v[j][e] = g;
+        }
+        if (s.M != nullptr) {
+            if constexpr (GRAM) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    mom[j][e] = s.sc.form == HPO_MUON_MOMENTUM_SUM ? s.sc.mu * mom[j][e] + v[j][e]
+                                                                    : s.sc.mu * mom[j][e] + s.sc.omu * v[j][e];
+                float* M = s.M + z * s.mbs + row[j] * s.mrs + col[j];
+                if (a.m_vec && cnt[j] >= 4) {
+                    *reinterpret_cast<f32x4_t*>(M) = mom[j];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e < cnt[j])
+                            M[e] = mom[j][e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[j][e] = nesterov_of(v[j][e], mom[j][e], s.sc);
+        }
+        /* 0 * inv_scale is 0 or, behind the edge of a NaN clip, not a number: edges are zeros */
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e >= cnt[j])
+                v[j][e] = 0.0f;
+    }
+}
+
+/* h and LO * l of eight values x * 2^e as 16-byte pieces. */
+template <int LO>
+__device__ __forceinline__ void split8(const float (&y)[8], u32x4_t& h, u32x4_t& l)
+{
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint32_t hb[2], lb[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float x = y[2 * w + e];
+            hb[e] = f16_bits(x);
+            lb[e] = f16_bits(static_cast<float>(LO) * (x - f16v(static_cast<uint16_t>(hb[e]))));
+        }
+        h[w] = hb[0] | (hb[1] << 16);
+        l[w] = lb[0] | (lb[1] << 16);
+    }
+}
+
+/* ---------------------------------------------------------------------- */
+/* S in parts                                                              */
+/* ---------------------------------------------------------------------- */
+/* grid (chunks, batch).  LDS: h and 2 l of an [MP][KC] tile.  MP = 128, 64:
+ * 2 x 2 wavefronts over the MP x MP result; MP = 32: every wavefront takes a
+ * quarter of the tile's columns for the whole result. */
+template <bool BF16, int MP, bool TALL>
+__global__ __launch_bounds__(kThreads, 2) void k_gram(GramArgs a)
+{
+    if (!gate_open(a.s.sc.gate))
+        return;
+    constexpr int KC = kTileElems / MP;
+    constexpr int kBytes = kTileElems * 2;
+    constexpr int kB = MP == 128 ? 2 : 1;               /* 32 x 32 blocks per wavefront and side */
+    constexpr bool kSplitK = MP == 32;
+    constexpr int kSlices = KC / 16 / (kSplitK ? 4 : 1);
+    __shared__ __attribute__((aligned(16))) char lds[2 * kBytes];
+    __shared__ uint32_t wave_top[4];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const GradVals gv = grad_vals(a.s.sc);
+    const int64_t z = blockIdx.y;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.run;
+    const int64_t c1 = c0 + a.run < a.n ? c0 + a.run : a.n;
+    const int r0 = kSplitK ? 0 : (wave >> 1) * 32 * kB, q0 = kSplitK ? 0 : (wave & 1) * 32 * kB;
+    const int s0 = kSplitK ? wave * kSlices : 0;
+    f32x16_t acc[kB][kB];
+#pragma unroll
+    for (int i = 0; i < kB; ++i)
+#pragma unroll
+        for (int j = 0; j < kB; ++j)
+            acc[i][j] = f32x16_t{};
+    int top = -1000;   /* the sums are scaled by 2^(2 (kTop - top)) */
+    using Sh = Share<MP, KC, !TALL>;
+    for (int64_t k0 = c0; k0 < c1; k0 += KC) {
+        f32x4_t v[8];
+        load_share<BF16, TALL, true, MP, KC>(a, gv, z, k0, v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t u = __float_as_uint(v[j][e]) & 0x7fffffffu;
+                m = u > m ? u : m;
+            }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t o = __shfl_xor(m, d, 64);
+            m = o > m ? o : m;
+        }
+        if (lane == 0)
+            wave_top[wave] = m;
+        __syncthreads();   /* also: the previous tile's fragments are read */
+        m = wave_top[0];
+#pragma unroll
+        for (int w = 1; w < 4; ++w)
+            m = wave_top[w] > m ? wave_top[w] : m;
+        /* every magnitude is under 2^e; inf and NaN stay what they are */
+        int e = -1000;
+        if (m >= 0x7f800000u)
+            e = 128;
+        else if (m != 0)
+            e = m >= 0x00800000u ? static_cast<int>(m >> 23) - 126 : -117 - __clz(static_cast<int>(m));
+        if (e > top) {
+            if (top > -1000) {
+                const int d = 2 * (top - e);
+#pragma unroll
+                for (int i = 0; i < kB; ++i)
+#pragma unroll
+                    for (int j = 0; j < kB; ++j)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            acc[i][j][r] = __builtin_ldexpf(acc[i][j][r], d);
+            }
+            top = e;
+        }
+        const int up = kTop - top;   /* no element is non-zero where top is still -1000 */
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float y[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                y[x] = __builtin_ldexpf(Sh::at(v, q, x), up);
+            u32x4_t h, l;
+            split8<2>(y, h, l);
+            int r, c;
+            Sh::piece(q, r, c);
+            const int off = piece_at<KC>(r, c / 8);
+            *reinterpret_cast<u32x4_t*>(lds + off) = h;
+            *reinterpret_cast<u32x4_t*>(lds + kBytes + off) = l;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < kSlices; ++s) {
+            u32x4_t fa[kB], fb[kB], fl[kB];
+#pragma unroll
+            for (int i = 0; i < kB; ++i) {
+                fa[i] = fragment<KC>(lds, r0 + 32 * i, s0 + s);
+                fb[i] = fragment<KC>(lds, q0 + 32 * i, s0 + s);
+                fl[i] = fragment<KC>(lds + kBytes, q0 + 32 * i, s0 + s);
+            }
+#pragma unroll
+            for (int i = 0; i < kB; ++i)
+#pragma unroll
+                for (int j = 0; j < kB; ++j) {
+                    acc[i][j] = mfma(fa[i], fb[j], acc[i][j]);
+                    acc[i][j] = mfma(fa[i], fl[j], acc[i][j]);
+                }
+        }
+    }
+    float* out = a.part + (z * a.chunks + blockIdx.x) * (MP * MP);
+    if (tid == 0)
+        a.part_exp[z * a.chunks + blockIdx.x] = top;
+    if constexpr (kSplitK) {
+        /* the four wavefronts' quarters, in order */
+        float* buf = reinterpret_cast<float*>(lds);
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+            buf[(wave * 16 + r) * 64 + lane] = acc[0][0][r];
+        __syncthreads();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int r = wave * 4 + x;
+            const float t = ((buf[r * 64 + lane] + buf[(16 + r) * 64 + lane]) + buf[(32 + r) * 64 + lane]) +
+                            buf[(48 + r) * 64 + lane];
+            out[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * MP + (lane & 31)] = t;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kB; ++i)
+#pragma unroll
+            for (int j = 0; j < kB; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    out[(r0 + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * MP + q0 + 32 * j + (lane & 31)] =
+                        acc[i][j][r];
+    }
+}
+
+/* ---------------------------------------------------------------------- */
+/* the steps in the m x m space                                            */
+/* ---------------------------------------------------------------------- */
+/* One workgroup per matrix (grid: batch), W x W wavefronts of B x B blocks.
+ * All operands are symmetric, so a matrix in LDS (rows of MP, h then l) serves
+ * as left and as right operand, and a lane's four consecutive rows of one
+ * column are stored as four consecutive columns of one row. */
+template <int MP>
+__global__ __launch_bounds__(MP == 32 ? 64 : 256) void k_gram_iterate(GramArgs a)
+{
+    if (!gate_open(a.s.sc.gate))
+        return;
+    constexpr int W = MP == 32 ? 1 : 2, B = MP / 32 / W;
+    constexpr int NT = 64 * W * W;
+    constexpr int kPlane = MP * MP * 2, kBuf = 2 * kPlane;
+    constexpr int kRaw = MP * (MP + 1) * 4;
+    __shared__ __attribute__((aligned(16))) char lds[2 * kBuf > kRaw ? 2 * kBuf : kRaw];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int r0 = (wave / W) * 32 * B, q0 = (wave % W) * 32 * B;
+    const int64_t z = blockIdx.x;
+    typedef f32x16_t Block[B][B];
+    auto row_of = [&](int i, int r) { return r0 + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3); };
+    auto col_of = [&](int j) { return q0 + 32 * j + (lane & 31); };
+
+    /* S: the parts at their largest exponent, in order */
+    const int32_t* pe = a.part_exp + z * a.chunks;
+    int top = -1000;
+    for (int c = 0; c < a.chunks; ++c)
+        top = pe[c] > top ? pe[c] : top;
+    Block A, P, Q, acc;
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            A[i][j] = f32x16_t{};
+    for (int c = 0; c < a.chunks; ++c) {
+        const float* part = a.part + (z * a.chunks + c) * (MP * MP);
+        const int d = 2 * (pe[c] - top);
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+#pragma unroll
+            for (int j = 0; j < B; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    A[i][j][r] += __builtin_ldexpf(part[row_of(i, r) * MP + col_of(j)], d);
+    }
+    /* (S + S^T) / 2 and the trace */
+    float* raw = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                raw[row_of(i, r) * (MP + 1) + col_of(j)] = A[i][j][r];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                A[i][j][r] = 0.5f * (A[i][j][r] + raw[col_of(j) * (MP + 1) + row_of(i, r)]);
+    /* every lane of every wavefront sums the same diagonal in the same order */
+    double trace = 0.0;
+    for (int i = lane; i < MP; i += 64)
+        trace += static_cast<double>(raw[i * (MP + 1) + i]);
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1)
+        trace += __shfl_xor(trace, off, 64);
+    __syncthreads();
+    /* d = ||g~|| + eps; the sums are at scale 2^(2 (kTop - top)) */
+    const double unit = ldexp(1.0, top > -1000 ? top - kTop : 0);
+    const float d = static_cast<float>(sqrt(trace) * unit) + a.s.sc.eps;
+    const double id = d == 0.0f ? 0.0 : 1.0 / static_cast<double>(d);
+    const double f = trace == 0.0 ? 0.0 : (unit * id) * (unit * id);
+    if (tid == 0) {
+        /* 1 / d as mantissa and exponent: it may lie beyond fp32's range */
+        int e = 0;
+        const double mant = frexp(id, &e);
+        a.inv[2 * z] = static_cast<float>(mant);
+        a.inv[2 * z + 1] = static_cast<float>(e + kTop);
+    }
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                A[i][j][r] = static_cast<float>(static_cast<double>(A[i][j][r]) * f);
+
+    char* b0 = lds;
+    char* b1 = lds + kBuf;
+    auto put = [&](char* buf, const Block& x, int e) {
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+#pragma unroll
+            for (int j = 0; j < B; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    /* rows row_of(i, 4 q) + 0..3 of column col_of(j), stored as that row's columns */
+                    uint32_t h[4], l[4];
+#pragma unroll
+                    for (int x4 = 0; x4 < 4; ++x4) {
+                        const float y = __builtin_ldexpf(x[i][j][4 * q + x4], e);
+                        h[x4] = f16_bits(y);
+                        l[x4] = f16_bits(y - f16v(static_cast<uint16_t>(h[x4])));
+                    }
+                    const int c = row_of(i, 4 * q);
+                    const int off = piece_at<MP>(col_of(j), c >> 3) + ((c >> 2) & 1) * 8;
+                    u32x2_t t;
+                    t.x = h[0] | (h[1] << 16);
+                    t.y = h[2] | (h[3] << 16);
+                    *reinterpret_cast<u32x2_t*>(buf + off) = t;
+                    t.x = l[0] | (l[1] << 16);
+                    t.y = l[2] | (l[3] << 16);
+                    *reinterpret_cast<u32x2_t*>(buf + kPlane + off) = t;
+                }
+    };
+    /* acc = x y * 2^-e */
+    auto mul = [&](const char* x, const char* y, Block& out, int e) {
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+#pragma unroll
+            for (int j = 0; j < B; ++j)
+                out[i][j] = f32x16_t{};
+#pragma unroll
+        for (int s = 0; s < MP / 16; ++s) {
+            u32x4_t xh[B], xl[B], yh[B], yl[B];
+#pragma unroll
+            for (int i = 0; i < B; ++i) {
+                xh[i] = fragment<MP>(x, r0 + 32 * i, s);
+                xl[i] = fragment<MP>(x + kPlane, r0 + 32 * i, s);
+                yh[i] = fragment<MP>(y, q0 + 32 * i, s);
+                yl[i] = fragment<MP>(y + kPlane, q0 + 32 * i, s);
+            }
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+#pragma unroll
+                for (int j = 0; j < B; ++j) {
+                    out[i][j] = mfma(xh[i], yh[j], out[i][j]);
+                    out[i][j] = mfma(xh[i], yl[j], out[i][j]);
+                    out[i][j] = mfma(xl[i], yh[j], out[i][j]);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+#pragma unroll
+            for (int j = 0; j < B; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    out[i][j][r] = __builtin_ldexpf(out[i][j][r], -e);
+    };
+
+    put(b0, A, a.step[0].a_exp);
+    __syncthreads();
+    for (int k = 0; k < a.steps; ++k) {
+        const GramStep& g = a.step[k];
+        const bool first = k == 0, last = k + 1 == a.steps;
+        mul(b0, b0, acc, 2 * g.a_exp);
+#pragma unroll
+        for (int i = 0; i < B; ++i)
+#pragma unroll
+            for (int j = 0; j < B; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const float q = g.b * A[i][j][r] + g.c * acc[i][j][r];
+                    Q[i][j][r] = row_of(i, r) == col_of(j) ? g.a + q : q;
+                }
+        if (first) {
+#pragma unroll
+            for (int i = 0; i < B; ++i)
+#pragma unroll
+                for (int j = 0; j < B; ++j)
+                    P[i][j] = Q[i][j];
+        }
+        if (first && last)
+            break;
+        put(b1, Q, g.q_exp);
+        __syncthreads();
+        if (!last)
+            mul(b1, b0, acc, g.q_exp + g.a_exp);   /* T = Q A */
+        if (!first) {
+            __syncthreads();
+            put(b0, P, g.p_exp);
+            __syncthreads();
+            mul(b1, b0, P, g.q_exp + g.p_exp);
+        }
+        if (!last) {
+            __syncthreads();
+            put(b0, acc, g.t_exp);
+            __syncthreads();
+            mul(b0, b1, A, g.t_exp + g.q_exp);     /* A = T Q */
+            __syncthreads();
+            put(b0, A, a.step[k + 1].a_exp);
+            __syncthreads();
+        }
+    }
+    /* P for the last pass: rows of 16-bit values, h then l */
+    uint16_t* out = a.P + z * (2 * MP * MP);
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float y = __builtin_ldexpf(P[i][j][r], a.p_exp);
+                const uint32_t h = f16_bits(y);
+                const int at = row_of(i, r) * MP + col_of(j);
+                out[at] = static_cast<uint16_t>(h);
+                out[MP * MP + at] = static_cast<uint16_t>(f16_bits(y - f16v(static_cast<uint16_t>(h))));
+            }
+    (void)NT;
+}
+
+/* ---------------------------------------------------------------------- */
+/* O = P X0                                                                */
+/* ---------------------------------------------------------------------- */
+/* grid (chunks, batch).  LDS: h and l of a [KC][MP] tile (X0's columns).  Each
+ * wavefront takes 32 rows of P (its fragments in registers) and two blocks of 32
+ * columns; the result of a tall matrix comes out transposed, so that lanes always
+ * run along its rows. */
+template <bool BF16, int MP, bool TALL>
+__global__ __launch_bounds__(kThreads, 2) void k_gram_apply(GramArgs a)
+{
+    if (!gate_open(a.s.sc.gate))
+        return;
+    constexpr int KC = kTileElems / MP;
+    constexpr int kBytes = kTileElems * 2;
+    constexpr int kSlices = MP / 16;
+    constexpr int kRowBlocks = MP / 32;
+    __shared__ __attribute__((aligned(16))) char lds[2 * kBytes];
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const GradVals gv = grad_vals(a.s.sc);
+    const int64_t z = blockIdx.y;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.run;
+    const int64_t c1 = c0 + a.run < a.n ? c0 + a.run : a.n;
+    const float mant = a.inv[2 * z];
+    const int ex = static_cast<int>(a.inv[2 * z + 1]);
+    const int i0 = (wave % kRowBlocks) * 32, j0 = (wave / kRowBlocks) * 64;
+    u32x4_t ph[kSlices], pl[kSlices];
+    const uint16_t* P = a.P + z * (2 * MP * MP);
+#pragma unroll
+    for (int s = 0; s < kSlices; ++s) {
+        const int at = (i0 + (lane & 31)) * MP + 16 * s + 8 * (lane >> 5);
+        ph[s] = *reinterpret_cast<const u32x4_t*>(P + at);
+        pl[s] = *reinterpret_cast<const u32x4_t*>(P + MP * MP + at);
+    }
+    using Sh = Share<KC, MP, TALL>;
+    for (int64_t k0 = c0; k0 < c1; k0 += KC) {
+        f32x4_t v[8];
+        load_share<BF16, TALL, false, KC, MP>(a, gv, z, k0, v);
+        __syncthreads();   /* the previous tile's fragments are read */
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float y[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const float g = Sh::at(v, q, x);
+                /* a stack of zeros with eps = 0 stays 0 */
+                y[x] = __builtin_ldexpf(g * mant, ex);
+            }
+            u32x4_t h, l;
+            split8<1>(y, h, l);
+            int r, c;
+            Sh::piece(q, r, c);
+            const int off = piece_at<MP>(r, c / 8);
+            *reinterpret_cast<u32x4_t*>(lds + off) = h;
+            *reinterpret_cast<u32x4_t*>(lds + kBytes + off) = l;
+        }
+        __syncthreads();
+        f32x16_t acc[2] = {f32x16_t{}, f32x16_t{}};
+#pragma unroll
+        for (int s = 0; s < kSlices; ++s) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const u32x4_t xh = fragment<MP>(lds, j0 + 32 * j, s);
+                const u32x4_t xl = fragment<MP>(lds + kBytes, j0 + 32 * j, s);
+                if constexpr (TALL) {
+                    acc[j] = mfma(xh, ph[s], acc[j]);
+                    acc[j] = mfma(xl, ph[s], acc[j]);
+                    acc[j] = mfma(xh, pl[s], acc[j]);
+                } else {
+                    acc[j] = mfma(ph[s], xh, acc[j]);
+                    acc[j] = mfma(ph[s], xl, acc[j]);
+                    acc[j] = mfma(pl[s], xh, acc[j]);
+                }
+            }
+        }
+        const int down = -(a.p_exp + kTop);
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int reg = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
+                const int64_t i = i0 + (TALL ? lane & 31 : reg);
+                const int64_t kk = k0 + j0 + 32 * j + (TALL ? reg : lane & 31);
+                if (i < a.m && kk < a.n)
+                    a.out[z * a.obs + (TALL ? kk * a.ors + i : i * a.ors + kk)] =
+                        static_cast<uint16_t>(bf16_rne_bits(__builtin_ldexpf(acc[j][r], down)));
+            }
+    }
+}
+
+template <typename... Args>
+hipError_t launch(void (*kernel)(Args...), dim3 grid, int block, hipStream_t stream, Args... args)
+{
+    void* argv[] = {static_cast<void*>(&args)...};
+    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(block), argv, 0, stream);
+}
+
+int mp_of(int64_t m) { return m <= 32 ? 32 : (m <= 64 ? 64 : 128); }
+
+struct GramPlan {
+    int mp;
+    int64_t m, n, run, chunks, count;
+    int64_t slot;   /* bytes of one matrix */
+};
+
+GramPlan gram_plan(int64_t batch, int64_t rows, int64_t cols)
+{
+    GramPlan p{};
+    p.m = rows > cols ? cols : rows;
+    p.n = rows > cols ? rows : cols;
+    p.mp = mp_of(p.m);
+    const int64_t kc = kTileElems / p.mp, tiles = (p.n + kc - 1) / kc;
+    /* enough workgroups to fill the chip twice; a run of 4 MP columns at the least keeps
+     * the partial results under a quarter of the gradient's bytes */
+    const int64_t least = 4 * p.mp / kc > 1 ? 4 * p.mp / kc : 1;
+    int64_t per = (tiles * batch + 511) / 512;
+    per = per < least ? least : per;
+    p.chunks = (tiles + per - 1) / per;
+    per = (tiles + p.chunks - 1) / p.chunks;
+    p.chunks = (tiles + per - 1) / per;
+    p.run = per * kc;
+    p.slot = (4 * p.chunks + 4) * p.mp * p.mp + 4 * p.chunks + 8;
+    constexpr int64_t kCap = int64_t{4} << 30;
+    const int64_t most = kCap / p.slot > 1 ? kCap / p.slot : 1;
+    const int64_t slices = (batch + most - 1) / most;
+    p.count = (batch + slices - 1) / slices;
+    return p;
+}
+
+template <bool BF16, int MP, bool TALL>
+hipError_t run(const GramArgs& a, uint32_t count, hipStream_t stream)
+{
+    const dim3 grid(static_cast<uint32_t>(a.chunks), count);
+    hipError_t e = launch(k_gram<BF16, MP, TALL>, grid, kThreads, stream, a);
+    if (e != hipSuccess)
+        return e;
+    e = launch(k_gram_iterate<MP>, dim3(count), MP == 32 ? 64 : 256, stream, a);
+    if (e != hipSuccess)
+        return e;
+    return launch(k_gram_apply<BF16, MP, TALL>, grid, kThreads, stream, a);
+}
+
+template <bool BF16, int MP>
+hipError_t run_tall(const GramArgs& a, bool tall, uint32_t count, hipStream_t stream)
+{
+    return tall ? run<BF16, MP, true>(a, count, stream) : run<BF16, MP, false>(a, count, stream);
+}
+
+template <bool BF16>
+hipError_t run_mp(const GramArgs& a, int mp, bool tall, uint32_t count, hipStream_t stream)
+{
+    if (mp == 32)
+        return run_tall<BF16, 32>(a, tall, count, stream);
+    if (mp == 64)
+        return run_tall<BF16, 64>(a, tall, count, stream);
+    return run_tall<BF16, 128>(a, tall, count, stream);
+}
+
+}  // namespace
+
+int64_t gram_workspace(int64_t batch, int64_t rows, int64_t cols)
+{
+    const GramPlan p = gram_plan(batch, rows, cols);
+    return p.count * p.slot;
+}
+
+hipError_t launch_gram(const OrthoArgs& o, hipStream_t stream)
+{
+    const GramPlan p = gram_plan(o.batch, o.rows, o.cols);
+    const bool tall = o.rows > o.cols;
+    for (int64_t z0 = 0; z0 < o.batch; z0 += p.count) {
+        const int64_t count = o.batch - z0 < p.count ? o.batch - z0 : p.count;
+        GramArgs a{};
+        a.s = slice_of(o, z0);
+        a.m = p.m;
+        a.n = p.n;
+        a.run = p.run;
+        a.chunks = static_cast<int32_t>(p.chunks);
+        a.g_vec = o.g_vec;
+        a.m_vec = o.m_vec;
+        char* at = static_cast<char*>(o.ws);
+        a.part = reinterpret_cast<float*>(at);
+        at += 4 * p.count * p.chunks * p.mp * p.mp;
+        a.P = reinterpret_cast<uint16_t*>(at);
+        at += 4 * p.count * p.mp * p.mp;
+        a.inv = reinterpret_cast<float*>(at);
+        at += 8 * p.count;
+        a.part_exp = reinterpret_cast<int32_t*>(at);
+        a.out = static_cast<uint16_t*>(o.out.data) + z0 * o.out.bs;
+        a.obs = o.out.bs;
+        a.ors = o.out.rs;
+        a.steps = o.steps;
+        a.p_exp = o.p_exp;
+        for (int k = 0; k < o.steps; ++k)
+            a.step[k] = o.gram[k];
+        const hipError_t e = o.g_bf16 ? run_mp<true>(a, p.mp, tall, static_cast<uint32_t>(count), stream)
+                                      : run_mp<false>(a, p.mp, tall, static_cast<uint32_t>(count), stream);
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+}  // namespace hpo

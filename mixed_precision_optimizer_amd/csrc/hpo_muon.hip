@@ -57,8 +57,7 @@
 
 #include <type_traits>
 
-#include "hpo_device.h"
-#include "hpo_stack_impl.h"
+#include "hpo_muon_device.h"
 
 namespace hpo {
 namespace {
@@ -139,53 +138,6 @@ using GenTile = NsTile<4, 2, 2, 2, HPO_NS_GEN_BK, HPO_NS_GEN_STAGES, 2>;
 using GenTile = SymTile;
 #endif
 constexpr int kTile = 64;              /* transpose tile of the input kernel */
-
-/* ---------------------------------------------------------------------- */
-/* gates and per-step values                                              */
-/* ---------------------------------------------------------------------- */
-__device__ __forceinline__ bool gate_open(const MuonGate& g)
-{
-    if (g.dev) {
-        /* the finalize has decided and counted the step (t = applied_steps, in the window) */
-        if (!g.st->applied)
-            return false;
-        const int64_t j = g.st->applied_steps - g.t_first;
-        return j >= 0 && j < g.window;
-    }
-    return !(g.d_found != nullptr && *g.d_found != 0);
-}
-
-struct GradVals {
-    float inv_scale;
-    float C;
-    bool clip;
-};
-
-/* Unscale factor and clip coefficient ([OPT-INFRA] §11.1): the same global
- * norm and rule as the AdamW update of the same step. */
-__device__ __forceinline__ GradVals grad_vals(const MuonScalars& sc)
-{
-    GradVals v;
-    float norm = 0.0f;
-    if (sc.gate.dev) {
-        v.inv_scale = sc.gate.st->step_inv_scale;
-        norm = sc.gate.st->grad_norm;
-    } else {
-        v.inv_scale = sc.inv_scale;
-        if (sc.max_norm > 0.0)
-            norm = *sc.d_norm;
-    }
-    v.clip = false;
-    v.C = 1.0f;
-    if (sc.max_norm > 0.0) {
-        const double c = sc.max_norm / (static_cast<double>(norm) + 1e-6);
-        if (c < 1.0) {
-            v.clip = true;
-            v.C = static_cast<float>(c);
-        }
-    }
-    return v;
-}
 
 /* ---------------------------------------------------------------------- */
 /* momentum + Nesterov gradient                                           */
@@ -397,13 +349,6 @@ __device__ __forceinline__ f32x16_t ns_mfma(bf16x8_t a, bf16x8_t b, f32x16_t c)
     else
         return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
-
-__device__ __forceinline__ uint32_t f16_bits(float x)
-{
-    return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
-}
-
-__device__ __forceinline__ float f16v(uint16_t b) { return static_cast<float>(__builtin_bit_cast(_Float16, b)); }
 
 struct GemmArgs {
     const uint16_t* P;
@@ -1321,33 +1266,6 @@ int64_t sum_parts(int64_t rows, int64_t cols)
     return p < 1 ? 1 : (p > kSumMax ? kSumMax : p);
 }
 
-struct OrthoSrc {
-    const void* G;
-    int64_t gbs, grs;
-    float* M;
-    int64_t mbs, mrs;
-    int64_t rows, cols;
-    MuonScalars sc;
-};
-
-template <bool BF16>
-__device__ __forceinline__ float src_at(const OrthoSrc& s, int64_t off)
-{
-    if constexpr (BF16)
-        return bf16_to_f32(static_cast<const uint16_t*>(s.G)[off]);
-    else
-        return static_cast<const float*>(s.G)[off];
-}
-
-/* g~ of one element from the stored grad and, when there is one, the momentum
- * after this step's update. */
-__device__ __forceinline__ float nesterov_of(float g, float M, const MuonScalars& sc)
-{
-    if (!sc.nesterov)
-        return M;
-    return sc.form == HPO_MUON_MOMENTUM_SUM ? g + sc.mu * M : sc.omu * g + sc.mu * M;
-}
-
 /* Momentum update in place and the partial sums of g~^2 (grid: parts, batch). */
 template <bool BF16>
 __global__ __launch_bounds__(kSumThreads) void k_stack_momentum(OrthoSrc s, double* part)
@@ -1522,17 +1440,7 @@ hipError_t ortho_slice(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64
     w.XL = take(xs);
     w.A = take(as);
     w.B = take(as);
-    OrthoSrc s{};
-    const int64_t esize = BF16 ? 2 : 4;
-    s.G = static_cast<const char*>(a.G.data) + esize * z0 * a.G.bs;
-    s.gbs = a.G.bs;
-    s.grs = a.G.rs;
-    s.M = a.M.data ? static_cast<float*>(a.M.data) + z0 * a.M.bs : nullptr;
-    s.mbs = a.M.bs;
-    s.mrs = a.M.rs;
-    s.rows = a.rows;
-    s.cols = a.cols;
-    s.sc = a.sc;
+    const OrthoSrc s = slice_of(a, z0);
     const uint32_t cnt = static_cast<uint32_t>(count);
     hipError_t e = launch3(k_stack_momentum<BF16>, dim3(static_cast<uint32_t>(p.parts), cnt), kSumThreads, stream, s,
                            w.part);

@@ -1,0 +1,121 @@
+/*
+ * hpo_muon_device.h -- device helpers shared by the Muon kernel files
+ * (hpo_muon.hip, hpo_gram.hip).  Not part of the public ABI.
+ *
+ * Source: [OPT-INFRA] "02 · Optimizer：算法与 infra" (llm-infra-atlas, train/02_optimizer).
+ */
+#ifndef HPO_MUON_DEVICE_H
+#define HPO_MUON_DEVICE_H
+
+#include <hip/hip_runtime.h>
+
+#include "hpo_device.h"
+#include "hpo_stack_impl.h"
+
+namespace hpo {
+namespace {
+
+/* ---------------------------------------------------------------------- */
+/* gates and per-step values                                              */
+/* ---------------------------------------------------------------------- */
+__device__ __forceinline__ bool gate_open(const MuonGate& g)
+{
+    if (g.dev) {
+        /* the finalize has decided and counted the step (t = applied_steps, in the window) */
+        if (!g.st->applied)
+            return false;
+        const int64_t j = g.st->applied_steps - g.t_first;
+        return j >= 0 && j < g.window;
+    }
+    return !(g.d_found != nullptr && *g.d_found != 0);
+}
+
+struct GradVals {
+    float inv_scale;
+    float C;
+    bool clip;
+};
+
+/* Unscale factor and clip coefficient ([OPT-INFRA] §11.1): the same global
+ * norm and rule as the AdamW update of the same step. */
+__device__ __forceinline__ GradVals grad_vals(const MuonScalars& sc)
+{
+    GradVals v;
+    float norm = 0.0f;
+    if (sc.gate.dev) {
+        v.inv_scale = sc.gate.st->step_inv_scale;
+        norm = sc.gate.st->grad_norm;
+    } else {
+        v.inv_scale = sc.inv_scale;
+        if (sc.max_norm > 0.0)
+            norm = *sc.d_norm;
+    }
+    v.clip = false;
+    v.C = 1.0f;
+    if (sc.max_norm > 0.0) {
+        const double c = sc.max_norm / (static_cast<double>(norm) + 1e-6);
+        if (c < 1.0) {
+            v.clip = true;
+            v.C = static_cast<float>(c);
+        }
+    }
+    return v;
+}
+
+/* ---------------------------------------------------------------------- */
+/* a stack's gradient and momentum                                         */
+/* ---------------------------------------------------------------------- */
+struct OrthoSrc {
+    const void* G;
+    int64_t gbs, grs;
+    float* M;
+    int64_t mbs, mrs;
+    int64_t rows, cols;
+    MuonScalars sc;
+};
+
+/* The matrices of a stack from z0 on. */
+inline OrthoSrc slice_of(const OrthoArgs& a, int64_t z0)
+{
+    OrthoSrc s{};
+    s.G = static_cast<const char*>(a.G.data) + (a.g_bf16 ? 2 : 4) * z0 * a.G.bs;
+    s.gbs = a.G.bs;
+    s.grs = a.G.rs;
+    s.M = a.M.data ? static_cast<float*>(a.M.data) + z0 * a.M.bs : nullptr;
+    s.mbs = a.M.bs;
+    s.mrs = a.M.rs;
+    s.rows = a.rows;
+    s.cols = a.cols;
+    s.sc = a.sc;
+    return s;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float src_at(const OrthoSrc& s, int64_t off)
+{
+    if constexpr (BF16)
+        return bf16_to_f32(static_cast<const uint16_t*>(s.G)[off]);
+    else
+        return static_cast<const float*>(s.G)[off];
+}
+
+/* g~ of one element from the stored grad and, when there is one, the momentum
+ * after this step's update. */
+__device__ __forceinline__ float nesterov_of(float g, float M, const MuonScalars& sc)
+{
+    if (!sc.nesterov)
+        return M;
+    return sc.form == HPO_MUON_MOMENTUM_SUM ? g + sc.mu * M : sc.omu * g + sc.mu * M;
+}
+
+__device__ __forceinline__ uint32_t f16_bits(float x)
+{
+    return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
+}
+
+__device__ __forceinline__ float f16v(uint16_t b) { return static_cast<float>(__builtin_bit_cast(_Float16, b)); }
+
+}  // namespace
+}  // namespace hpo
+
+#endif /* HPO_MUON_DEVICE_H */

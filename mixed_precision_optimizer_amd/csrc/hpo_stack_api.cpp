@@ -167,6 +167,18 @@ double quadratic_max(double b, double c, double L)
     return best;
 }
 
+/* Largest |a + b l + c l^2| over 0 <= l <= L. */
+double shifted_max(double a, double b, double c, double L)
+{
+    double best = std::max(std::fabs(a), std::fabs(a + L * (b + c * L)));
+    if (c != 0.0) {
+        const double x = -b / (2.0 * c);
+        if (x > 0.0 && x < L)
+            best = std::max(best, std::fabs(a + x * (b + c * x)));
+    }
+    return best;
+}
+
 /* The exponent e with bound * 2^e in (2^13, 2^14]: a factor of four below
  * fp16's largest value is left for roundings; zero bounds take 0. */
 int fit(double bound)
@@ -186,6 +198,7 @@ hpo_status ns_scales(const hpo_muon_cfg* cfg, hpo::OrthoArgs& out)
     double S = 1.0;
     out.steps = cfg->ns_steps;
     int ex = fit(S);
+    double Pb = 1.0;   /* bound of the product of the steps' Q */
     out.x0_scale = static_cast<float>(std::ldexp(1.0, ex));
     for (int32_t k = 0; k < cfg->ns_steps; ++k) {
         const double* c = cfg->ns_coeffs ? cfg->ns_coeffs + 3 * k : kDefault;
@@ -203,9 +216,23 @@ hpo_status ns_scales(const hpo_muon_cfg* cfg, hpo::OrthoArgs& out)
         s.poly_c = static_cast<float>(std::ldexp(static_cast<double>(static_cast<float>(c[2])), eb - 2 * ea));
         s.step_a = static_cast<float>(std::ldexp(static_cast<double>(static_cast<float>(c[0])), en - ex));
         s.step_c = static_cast<float>(std::ldexp(1.0, en - eb - ex));
+        const double Qb = shifted_max(c[0], c[1], c[2], L);
+        hpo::GramStep& q = out.gram[k];
+        q.a = static_cast<float>(c[0]);
+        q.b = static_cast<float>(c[1]);
+        q.c = static_cast<float>(c[2]);
+        q.a_exp = fit(L);
+        q.q_exp = fit(Qb);
+        q.t_exp = fit(Qb * L);
+        q.p_exp = fit(Pb);
+        Pb *= std::max(Qb, 1e-6);
         S = std::max(next, 1e-6);
         ex = en;
     }
+    out.p_exp = fit(Pb);
+    /* P is held to 2^-22 of its bound: up to 2^11 of growth (the default coefficients' six
+     * steps) that is far below the result's rounding */
+    out.use_gram = Pb <= 2048.0 ? 1 : 0;
     return HPO_OK;
 }
 
@@ -264,6 +291,8 @@ hpo_status hpo_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols
     if (rows > 0 && cols > (int64_t{1} << 40) / rows)
         return fail(HPO_EINVAL, "matrices of %lld x %lld are too large (2^40 elements)", (long long)rows, (long long)cols);
     *out_bytes = batch == 0 || rows == 0 || cols == 0 ? 0 : hpo::ortho_workspace(batch, rows, cols);
+    if (*out_bytes != 0 && std::min(rows, cols) <= hpo::kGramMax)   /* either form, as the coefficients allow */
+        *out_bytes = std::max(*out_bytes, hpo::gram_workspace(batch, rows, cols));
     return ok();
 }
 
@@ -316,6 +345,9 @@ hpo_status hpo_orthogonalize(const hpo_stack* G, const hpo_stack* momentum, cons
     a.M = view(momentum);
     a.out = view(out);
     a.g_bf16 = G->dtype == HPO_PARAM_BF16 ? 1 : 0;
+    a.g_vec = rows_vec4(G) ? 1 : 0;
+    a.m_vec = momentum && rows_vec4(momentum) ? 1 : 0;
+    a.use_gram = a.use_gram && std::min(G->rows, G->cols) <= hpo::kGramMax ? 1 : 0;
     a.batch = G->batch;
     a.rows = G->rows;
     a.cols = G->cols;
@@ -329,7 +361,7 @@ hpo_status hpo_orthogonalize(const hpo_stack* G, const hpo_stack* momentum, cons
     a.sc.form = cfg->momentum_form;
     a.sc.nesterov = cfg->nesterov;
     a.ws = d_workspace;
-    const hipError_t e = hpo::launch_orthogonalize(a, as_stream(stream));
+    const hipError_t e = a.use_gram ? hpo::launch_gram(a, as_stream(stream)) : hpo::launch_orthogonalize(a, as_stream(stream));
     if (e != hipSuccess)
         return hip_fail(e, "launch Newton-Schulz of a stack");
     return ok();

@@ -100,9 +100,24 @@ struct NsStepScale {
     float step_a, step_c; /* Y = step_a * X' + step_c * (B' X'), Y = X of the next step at its scale (last: 1) */
 };
 
+/* One step in the space of the Gram matrix: coefficients, and the exponents
+ * at which A, Q = a I + b A + c A^2, T = Q A and P (the product of the earlier Q)
+ * are split into two fp16 values. */
+struct GramStep {
+    float a, b, c;
+    int32_t a_exp, q_exp, t_exp, p_exp;
+};
+
+/* Short sides up to this take the Gram form. */
+constexpr int64_t kGramMax = 128;
+
 struct OrthoArgs {
     StackView G, M, out;   /* M.data NULL: no momentum */
     int32_t g_bf16;
+    int32_t g_vec, m_vec;  /* rows take 4-element accesses */
+    int32_t use_gram;      /* the short side fits and P stays in range */
+    int32_t p_exp;         /* exponent of the final P */
+    GramStep gram[HPO_NS_MAX_STEPS];
     int32_t steps;
     int64_t batch, rows, cols;
     MuonScalars sc;        /* gate, inv_scale, clip, momentum, eps */
@@ -112,6 +127,8 @@ struct OrthoArgs {
 };
 
 int64_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols);
+int64_t gram_workspace(int64_t batch, int64_t rows, int64_t cols);
+hipError_t launch_gram(const OrthoArgs& a, hipStream_t stream);
 hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t stream);
 
 }  // namespace hpo
