@@ -110,7 +110,8 @@ struct NsTile {
     static_assert(kChunks % kWaves == 0, "stage chunks split evenly over the wavefronts");
     static_assert(STAGES >= 2, "at least double buffering");
     static_assert(kNsPad % kBM == 0 && kNsPad % kBN == 0 && kNsPad % BK == 0, "padding covers the tiles");
-    static_assert(kBM == 256 && (kBN == 256 || kBN == 128), "the epilogue's thread maps");
+    static_assert(kBM == 256 ? kBN == 256 || kBN == 128 : kBM == kBN && (kBM == 128 || kBM == 64),
+                  "the epilogue's thread maps");
     static_assert(kLdsBytes * WG <= 160 * 1024, "the workgroups of a CU fit its LDS");
 };
 /* Symmetric outputs (A = XX^T, B = bA + cAA^T) mirror whole tiles: square,
@@ -137,6 +138,11 @@ using GenTile = NsTile<4, 2, 2, 2, HPO_NS_GEN_BK, HPO_NS_GEN_STAGES, 2>;
 #else
 using GenTile = SymTile;
 #endif
+/* The stack's iteration on grids too small to fill the chip with 256 x 256
+ * tiles: 128 x 128 tiles of four wavefronts (two workgroups per CU), and 64 x 64
+ * tiles with loads running three stages ahead. */
+using MidTile = NsTile<2, 2, 2, 2, 64, 2, 2>;
+using SmallTile = NsTile<2, 2, 1, 1, 64, 4, 2>;
 constexpr int kTile = 64;              /* transpose tile of the input kernel */
 
 /* ---------------------------------------------------------------------- */
@@ -369,9 +375,9 @@ struct GemmArgs {
     float a, b, c;
     int64_t R, Cn;       /* update / out: natural shape; the C tile is in natural orientation */
     float* out;          /* out epilogue */
-    uint16_t* XL;        /* f16 step: what the rounding of X lost (as XS lies; NULL: not kept), read ... */
-    uint16_t* XLn;       /* ... and written, in place (NULL: not wanted by the next step) */
-    int64_t ldxl, sxl;
+    uint16_t* XL;        /* f16 step: what the rounding of X lost, as lo_at() lays it out */
+    int64_t sxl;
+    int32_t lo_out;      /* f16 step: the next step wants it (written in place) */
     uint16_t* out16;     /* f16 out: bf16 result */
     int64_t oss, ors;    /* its matrix and row strides */
     const TensorDesc* desc;
@@ -663,7 +669,7 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
         using F0 = std::integral_constant<int, 0>;
         using F1 = std::integral_constant<int, 1>;
         fload(0, 0, F0{});
-        /* nk is even and at least 4 (K is a multiple of 256): two stages per
+        /* nk is even and at least 2 (K is a multiple of 128): two stages per
          * trip, so that each stage's buffer index is a constant, and the last two
          * stages peeled, so that no branch inside the loop splits the
          * accumulators' live range.  kMode: 0 a stage that loads stage kt + 2,
@@ -770,9 +776,18 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
         constexpr int kCPR = kBM / 8;                        /* 16-byte chunks per tile column */
         constexpr int kEpiPieces = kBN * kCPR / kNsThreads;  /* 16-byte pieces per thread */
         constexpr int kJB = kBN / 8;                         /* 8-column blocks per tile row */
-        constexpr int kBlocks = (kBM / 4) * kJB / kNsThreads;   /* 4 x 8 blocks per thread */
-        static_assert(kEpiPieces * kNsThreads == kBN * kCPR && kBlocks * kNsThreads == (kBM / 4) * kJB, "whole pieces");
-        static_assert(kCPR >= 16 && (kJB == 16 || kJB == 32), "bank maps");
+        constexpr int kAllBlocks = (kBM / 4) * kJB;          /* 4 x 8 blocks of the tile */
+        constexpr int kBlocks = (kAllBlocks + kNsThreads - 1) / kNsThreads;   /* per thread */
+        constexpr int kJLow = kJB < 16 ? kJB : 16;           /* column blocks that neighbouring threads take */
+        static_assert(kEpiPieces * kNsThreads == kBN * kCPR, "whole pieces");
+        static_assert(kAllBlocks % kNsThreads == 0 || kAllBlocks < kNsThreads, "whole blocks");
+        static_assert(kCPR >= 8 && (kJB == 8 || kJB == 16 || kJB == 32), "bank maps");
+        auto block_of = [](int bidx, int& i0, int& j0) {
+            const int rest = bidx / (2 * kJLow);
+            const int par = bidx & 1, jb = ((bidx >> 1) & (kJLow - 1)) | ((rest % (kJB / kJLow)) << 4);
+            i0 = 8 * (rest / (kJB / kJLow)) + 4 * par;
+            j0 = 8 * jb;
+        };
         uint16_t* Tt = reinterpret_cast<uint16_t*>(lds);
         float* T32 = reinterpret_cast<float*>(lds);
         /* element offset of C[i][j] */
@@ -808,9 +823,10 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
 #pragma clang loop unroll(full)
             for (int k = 0; k < kBlocks; ++k) {
                 const int bidx = tid + k * kNsThreads;
-                const int rest = bidx >> 5;
-                const int par = bidx & 1, jb = ((bidx >> 1) & 15) | ((rest % (kJB / 16)) << 4), ic = rest / (kJB / 16);
-                const int i0 = 8 * ic + 4 * par, j0 = 8 * jb;
+                if (kAllBlocks < kNsThreads && bidx >= kAllBlocks)
+                    continue;
+                int i0, j0;
+                block_of(bidx, i0, j0);
                 u32x2_t v[8];
 #pragma clang loop unroll(full)
                 for (int e = 0; e < 8; ++e)
@@ -922,60 +938,47 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
             store_n(g.X + z * g.sx + row0 * g.ldx + col0, g.ldx);
             store_t(g.XT + z * g.sxt + col0 * g.ldxt + row0, g.ldxt);
         } else if constexpr (EPI == kEpiF16Step) {
-            /* acc becomes x; each thread reads and writes the tile's elements it holds */
-            auto each = [&](auto&& f) {
-#pragma clang loop unroll(full)
-                for (int ti = 0; ti < kTM; ++ti)
-#pragma clang loop unroll(full)
-                    for (int tj = 0; tj < kTN; ++tj) {
-#pragma clang loop unroll(full)
-                        for (int q = 0; q < 4; ++q) {
-                            const int i = wm + 32 * ti + 8 * q + lrow4, j = wn + 32 * tj + lcol;
-                            f(acc[ti][tj], 4 * q, reinterpret_cast<u32x2_t*>(Tt + tt(j, i)));
-                        }
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
-            };
+            /* what the rounding lost lies in the order of these registers: each thread reads
+             * (and overwrites) what the same thread wrote a step ago */
+            u32x2_t* lo = reinterpret_cast<u32x2_t*>(g.XL + z * g.sxl) +
+                          ((ty * g.nx + tx) * T::kWaves + wave) * (kTM * kTN * 4 * 64) + lane;
+            const float al = g.a * (1.0f / kLoScale);
             stage_in(g.XS + z * g.sxs + col0 * g.ldxs + row0, g.ldxs);
             __syncthreads();
-            each([&](f32x16_t& v, int r, u32x2_t* pt) {
-                const u32x2_t xv = *pt;
 #pragma clang loop unroll(full)
-                for (int e = 0; e < 4; ++e) {
-                    const float ax = g.a * unpack(xv, e), cx = g.c * v[r + e];
-                    v[r + e] = ax + cx;
-                }
-            });
-            if (g.XL != nullptr) {
-                const float al = g.a * (1.0f / kLoScale);
-                __syncthreads();
-                stage_in(g.XL + z * g.sxl + col0 * g.ldxl + row0, g.ldxl);
-                __syncthreads();
-                each([&](f32x16_t& v, int r, u32x2_t* pt) {
-                    const u32x2_t xv = *pt;
+            for (int ti = 0; ti < kTM; ++ti)
 #pragma clang loop unroll(full)
-                    for (int e = 0; e < 4; ++e) {
-                        const float lx = al * unpack(xv, e);
-                        v[r + e] = v[r + e] + lx;
+                for (int tj = 0; tj < kTN; ++tj) {
+                    u32x2_t lv[4];
+#pragma clang loop unroll(full)
+                    for (int q = 0; q < 4; ++q)
+                        lv[q] = lo[((ti * kTN + tj) * 4 + q) * 64];
+#pragma clang loop unroll(full)
+                    for (int q = 0; q < 4; ++q) {
+                        const int i = wm + 32 * ti + 8 * q + lrow4, j = wn + 32 * tj + lcol;
+                        u32x2_t* pt = reinterpret_cast<u32x2_t*>(Tt + tt(j, i));
+                        const u32x2_t xv = *pt;
+                        float x[4];
+#pragma clang loop unroll(full)
+                        for (int e = 0; e < 4; ++e) {
+                            const float ax = g.a * unpack(xv, e), lx = al * unpack(lv[q], e);
+                            const float cx = g.c * acc[ti][tj][4 * q + e];
+                            x[e] = (ax + lx) + cx;
+                        }
+                        const u32x2_t h = pack4(x[0], x[1], x[2], x[3]);
+                        *pt = h;
+                        if (g.lo_out) {
+#pragma clang loop unroll(full)
+                            for (int e = 0; e < 4; ++e)
+                                x[e] = (x[e] - unpack(h, e)) * kLoScale;
+                            lo[((ti * kTN + tj) * 4 + q) * 64] = pack4(x[0], x[1], x[2], x[3]);
+                        }
                     }
-                });
-            }
-            each([&](f32x16_t& v, int r, u32x2_t* pt) { *pt = pack4(v[r], v[r + 1], v[r + 2], v[r + 3]); });
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             __syncthreads();
             store_n(g.X + z * g.sx + row0 * g.ldx + col0, g.ldx);
             store_t(g.XT + z * g.sxt + col0 * g.ldxt + row0, g.ldxt);
-            if (g.XLn != nullptr) {
-                __syncthreads();
-                each([&](f32x16_t& v, int r, u32x2_t* pt) {
-                    float l[4];
-#pragma clang loop unroll(full)
-                    for (int e = 0; e < 4; ++e)
-                        l[e] = (v[r + e] - f16v(static_cast<uint16_t>(f16_bits(v[r + e])))) * kLoScale;
-                    *pt = pack4(l[0], l[1], l[2], l[3]);
-                });
-                __syncthreads();
-                store_t(g.XLn + z * g.sxl + col0 * g.ldxl + row0, g.ldxl);
-            }
         } else if constexpr (EPI == kEpiF16Out) {
             stage_in(g.XS + z * g.sxs + col0 * g.ldxs + row0, g.ldxs);
             __syncthreads();
@@ -1008,9 +1011,10 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
 #pragma clang loop unroll(full)
             for (int k = 0; k < kBlocks; ++k) {
                 const int bidx = tid + k * kNsThreads;
-                const int rest = bidx >> 5;
-                const int par = bidx & 1, jb = ((bidx >> 1) & 15) | ((rest % (kJB / 16)) << 4), ic = rest / (kJB / 16);
-                const int i0 = 8 * ic + 4 * par, j0 = 8 * jb;
+                if (kAllBlocks < kNsThreads && bidx >= kAllBlocks)
+                    continue;
+                int i0, j0;
+                block_of(bidx, i0, j0);
                 const int64_t nc = col0 + j0;
                 if (nc >= g.Cn)
                     continue;
@@ -1306,14 +1310,33 @@ __global__ __launch_bounds__(kSumThreads) void k_stack_momentum(OrthoSrc s, doub
         part[z * gridDim.x + blockIdx.x] = tot;
 }
 
+/* Where the low parts of rows i .. i + 3 (i a multiple of 8; rows i + 4 .. i + 7 are 32
+ * further on) of column j lie, in units of four values: tile by tile of the step's
+ * GEMM, then in the order of its accumulator registers. */
+template <class T>
+__device__ __forceinline__ int64_t lo_at_tile(int64_t i, int64_t j, int64_t np)
+{
+    const int64_t tile = (i / T::kBM) * (np / T::kBN) + j / T::kBN;
+    const int li = static_cast<int>(i % T::kBM), lj = static_cast<int>(j % T::kBN);
+    const int wave = li / (32 * T::kTM) * T::kWavesN + lj / (32 * T::kTN);
+    const int ti = li / 32 % T::kTM, tj = lj / 32 % T::kTN, q = li % 32 / 8;
+    return (((tile * T::kWaves + wave) * T::kTM + ti) * T::kTN + tj) * 256 + q * 64 + lj % 32;
+}
+
+__device__ __forceinline__ int64_t lo_at(int32_t tile, int64_t i, int64_t j, int64_t np)
+{
+    return tile == GenTile::kBM ? lo_at_tile<GenTile>(i, j, np)
+                                : (tile == MidTile::kBM ? lo_at_tile<MidTile>(i, j, np) : lo_at_tile<SmallTile>(i, j, np));
+}
+
 /* X0 = f16(g~ / (norm + eps) * 2^ex) both ways round, zero-padded, and what the
- * rounding lost in the X^T orientation (grid: padded columns / 64, rows / 64,
- * batch; natural orientation, as k_muon_ns_input). */
+ * rounding lost (grid: padded columns / 64, rows / 64, batch; natural
+ * orientation, as k_muon_ns_input). */
 template <bool BF16>
 __global__ __launch_bounds__(kBlock) void k_stack_input(OrthoSrc s, const double* part, int32_t parts, float x0_scale,
                                                         uint16_t* copy, int64_t ld_copy, uint16_t* trans,
                                                         int64_t ld_trans, int64_t stride, uint16_t* lo,
-                                                        int32_t lo_trans)
+                                                        int32_t lo_tile, int32_t tall)
 {
     if (!gate_open(s.sc.gate))
         return;
@@ -1379,12 +1402,20 @@ __global__ __launch_bounds__(kBlock) void k_stack_input(OrthoSrc s, const double
         const int r = e / 8, p = (e % 8) * 8;
         *reinterpret_cast<u32x4_t*>(copy + z * stride + (r0 + r) * ld_copy + c0 + p) = row8(tile, r, p);
         *reinterpret_cast<u32x4_t*>(trans + z * stride + (c0 + r) * ld_trans + r0 + p) = col8(tile, r, p);
-        if (lo != nullptr) {
-            if (lo_trans)
-                *reinterpret_cast<u32x4_t*>(lo + z * stride + (c0 + r) * ld_trans + r0 + p) = col8(tlo, r, p);
-            else
-                *reinterpret_cast<u32x4_t*>(lo + z * stride + (r0 + r) * ld_copy + c0 + p) = row8(tlo, r, p);
-        }
+    }
+    if (lo == nullptr)
+        return;
+    /* eight consecutive rows of one column of the wide form, column fastest over the threads */
+#pragma unroll
+    for (int q = 0; q < kTile * kTile / 8 / kBlock; ++q) {
+        const int e = tid + q * kBlock;
+        const int j = e % kTile, p = (e / kTile) * 8;
+        const u32x4_t v = tall ? row8(tlo, j, p) : col8(tlo, j, p);
+        const int64_t wi = (tall ? c0 : r0) + p, wj = (tall ? r0 : c0) + j;   /* wide coordinates */
+        const int64_t ld = tall ? ld_copy : ld_trans;                         /* mp; np = stride / mp */
+        u32x2_t* dst = reinterpret_cast<u32x2_t*>(lo + z * stride) + lo_at(lo_tile, wi, wj, stride / ld);
+        dst[0] = u32x2_t{v.x, v.y};
+        dst[32] = u32x2_t{v.z, v.w};
     }
 }
 
@@ -1399,15 +1430,22 @@ struct OrthoPlan {
     int64_t parts;
     int64_t slot;      /* bytes of one matrix */
     int64_t count;     /* matrices of a slice */
+    int32_t tile;      /* GEMM tile side */
 };
+
+int64_t pad_to(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
 OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols)
 {
     OrthoPlan p{};
     p.m = rows > cols ? cols : rows;
     p.n = rows > cols ? rows : cols;
-    p.mp = ns_pad(p.m);
-    p.np = ns_pad(p.n);
+    /* the largest tile whose grid (of the step's product) still gives every CU a workgroup */
+    auto grid = [&](int64_t t) { return batch * (pad_to(p.m, t) / t) * (pad_to(p.n, t) / t); };
+    constexpr int64_t kCus = 256;
+    p.tile = grid(GenTile::kBM) >= kCus ? GenTile::kBM : (grid(MidTile::kBM) >= kCus ? MidTile::kBM : SmallTile::kBM);
+    p.mp = pad_to(p.m, p.tile);
+    p.np = pad_to(p.n, p.tile);
     p.parts = sum_parts(rows, cols);
     p.slot = 2 * (4 * p.mp * p.np + 2 * p.mp * p.mp);
     /* slices of equal size under the cap (one matrix at the least) */
@@ -1420,7 +1458,7 @@ OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols)
 
 int64_t round256(int64_t x) { return (x + 255) / 256 * 256; }
 
-template <bool BF16>
+template <bool BF16, class T>
 hipError_t ortho_slice(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64_t count, hipStream_t stream)
 {
     const bool tall = a.rows > a.cols;
@@ -1452,8 +1490,8 @@ hipError_t ortho_slice(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64
     e = launch3(k_stack_input<BF16>,
                 dim3(static_cast<uint32_t>(Cp / kTile), static_cast<uint32_t>(Rp / kTile), cnt), kBlock, stream, s,
                 static_cast<const double*>(w.part), static_cast<int32_t>(p.parts), a.x0_scale, tall ? w.XT[0] : w.X,
-                tall ? p.mp : p.np, tall ? w.X : w.XT[0], tall ? p.np : p.mp, xs, lo0 ? w.XL : nullptr,
-                static_cast<int32_t>(tall ? 0 : 1));
+                tall ? p.mp : p.np, tall ? w.X : w.XT[0], tall ? p.np : p.mp, xs, lo0 ? w.XL : nullptr, p.tile,
+                static_cast<int32_t>(tall ? 1 : 0));
     if (e != hipSuccess)
         return e;
     const MuonUpdate up{};
@@ -1468,9 +1506,9 @@ hipError_t ortho_slice(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64
         g.K = static_cast<int32_t>(p.np);
         g.C = w.A; g.ldc = p.mp; g.sc = as;
         g.c = f.gram;
-        g.nt = static_cast<int32_t>(p.mp / SymTile::kBM);
+        g.nt = static_cast<int32_t>(p.mp / T::kBM);
         const dim3 tri(static_cast<uint32_t>(g.nt * (g.nt + 1) / 2), 1, cnt);
-        e = launch3(k_ns_gemm<kEpiF16Gram, true, SymTile>, tri, SymTile::kThreads, stream, g, up);
+        e = launch3(k_ns_gemm<kEpiF16Gram, true, T>, tri, T::kThreads, stream, g, up);
         if (e != hipSuccess)
             return e;
         g.P = w.A; g.ldp = p.mp; g.sp = as;
@@ -1479,7 +1517,7 @@ hipError_t ortho_slice(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64
         g.C = w.B;
         g.b = f.poly_b;
         g.c = f.poly_c;
-        e = launch3(k_ns_gemm<kEpiF16Poly, true, SymTile>, tri, SymTile::kThreads, stream, g, up);
+        e = launch3(k_ns_gemm<kEpiF16Poly, true, T>, tri, T::kThreads, stream, g, up);
         if (e != hipSuccess)
             return e;
         g.P = w.B; g.ldp = p.mp; g.sp = as;
@@ -1487,17 +1525,16 @@ hipError_t ortho_slice(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64
         g.X = w.X; g.ldx = p.np; g.sx = xs;
         g.XT = w.XT[cur ^ 1]; g.ldxt = p.mp; g.sxt = xs;
         g.XS = w.XT[cur]; g.ldxs = p.mp; g.sxs = xs;
-        g.ldxl = p.mp;
+        g.XL = w.XL;
         g.sxl = xs;
+        g.lo_out = k + 2 < a.steps ? 1 : 0;
         g.a = f.step_a;
         g.c = f.step_c;
-        g.nx = static_cast<int32_t>(p.np / GenTile::kBN);
-        g.ny = static_cast<int32_t>(p.mp / GenTile::kBM);
+        g.nx = static_cast<int32_t>(p.np / T::kBN);
+        g.ny = static_cast<int32_t>(p.mp / T::kBM);
         if (!last) {
-            g.XL = w.XL;
-            g.XLn = k + 2 < a.steps ? w.XL : nullptr;
-            e = launch3(k_ns_gemm<kEpiF16Step, false, GenTile>, dim3(static_cast<uint32_t>(g.nx * g.ny), 1, cnt),
-                        GenTile::kThreads, stream, g, up);
+            e = launch3(k_ns_gemm<kEpiF16Step, false, T>, dim3(static_cast<uint32_t>(g.nx * g.ny), 1, cnt),
+                        T::kThreads, stream, g, up);
         } else {
             g.R = p.m;
             g.Cn = p.n;
@@ -1505,22 +1542,33 @@ hipError_t ortho_slice(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64
                 g.P = w.XT[cur]; g.ldp = p.mp; g.sp = xs;
                 g.Q = w.B; g.ldq = p.mp; g.sq = as;
                 g.XS = w.X; g.ldxs = p.np; g.sxs = xs;
-                g.nx = static_cast<int32_t>(p.mp / GenTile::kBN);
-                g.ny = static_cast<int32_t>(p.np / GenTile::kBM);
+                g.nx = static_cast<int32_t>(p.mp / T::kBN);
+                g.ny = static_cast<int32_t>(p.np / T::kBM);
                 g.R = p.n;
                 g.Cn = p.m;
             }
             g.out16 = static_cast<uint16_t*>(a.out.data) + z0 * a.out.bs;
             g.oss = a.out.bs;
             g.ors = a.out.rs;
-            e = launch3(k_ns_gemm<kEpiF16Out, false, GenTile>, dim3(static_cast<uint32_t>(g.nx * g.ny), 1, cnt),
-                        GenTile::kThreads, stream, g, up);
+            e = launch3(k_ns_gemm<kEpiF16Out, false, T>, dim3(static_cast<uint32_t>(g.nx * g.ny), 1, cnt),
+                        T::kThreads, stream, g, up);
         }
         if (e != hipSuccess)
             return e;
         cur ^= 1;
     }
     return hipSuccess;
+}
+
+template <bool BF16>
+hipError_t ortho_tiles(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64_t count, hipStream_t stream)
+{
+    static_assert(std::is_same_v<SymTile, GenTile>, "one padding for both kinds of product");
+    if (p.tile == GenTile::kBM)
+        return ortho_slice<BF16, GenTile>(a, p, z0, count, stream);
+    if (p.tile == MidTile::kBM)
+        return ortho_slice<BF16, MidTile>(a, p, z0, count, stream);
+    return ortho_slice<BF16, SmallTile>(a, p, z0, count, stream);
 }
 
 }  // namespace
@@ -1536,8 +1584,8 @@ hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t stream)
     const OrthoPlan p = ortho_plan(a.batch, a.rows, a.cols);
     for (int64_t z = 0; z < a.batch; z += p.count) {
         const int64_t count = a.batch - z < p.count ? a.batch - z : p.count;
-        const hipError_t e = a.g_bf16 ? ortho_slice<true>(a, p, z, count, stream)
-                                      : ortho_slice<false>(a, p, z, count, stream);
+        const hipError_t e = a.g_bf16 ? ortho_tiles<true>(a, p, z, count, stream)
+                                      : ortho_tiles<false>(a, p, z, count, stream);
         if (e != hipSuccess)
             return e;
     }
