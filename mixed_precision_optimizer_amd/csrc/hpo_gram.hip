@@ -34,6 +34,8 @@ namespace hpo {
 namespace {
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
@@ -47,7 +49,8 @@ struct GramArgs {
     OrthoSrc s;
     int64_t m, n;        /* short and long side */
     int64_t run;         /* columns (of the wide form) a workgroup takes, whole tiles */
-    int32_t chunks;      /* workgroups per matrix */
+    int64_t apply_run;   /* the same for the last pass */
+    int32_t chunks;      /* workgroups per matrix of the first */
     int32_t g_vec;       /* rows of G, M and out take 4-element accesses */
     int32_t m_vec;
     int32_t o_vec;
@@ -164,88 +167,117 @@ struct Share {
     }
 };
 
-/* g~ of a share.  LDS row = short side (GRAM) or long side (apply); UPDATE
- * writes the momentum, else it is read as it is after the update. */
-template <bool BF16, bool TALL, bool GRAM, int LROW, int LCOL>
-__device__ __forceinline__ void load_share(const GramArgs& a, const GradVals& k, int64_t z, int64_t k0, f32x4_t (&v)[8])
+/* The stored elements of a share. */
+struct Raw {
+    f32x4_t g[8], m[8];
+};
+
+/* A share's elements in memory: LDS row = short side (GRAM) or long side
+ * (apply), columns of the wide form from k0 on. */
+template <bool TALL, bool GRAM, int LROW, int LCOL>
+__device__ __forceinline__ void place(const OrthoSrc& s, int64_t k0, int j, int64_t& row, int64_t& col, int& cnt)
 {
-    constexpr bool kAlong = GRAM != TALL;   /* LDS columns run along memory */
-    using Sh = Share<LROW, LCOL, kAlong>;
+    int r, c;
+    Share<LROW, LCOL, GRAM != TALL>::run(j, r, c);
+    const int64_t i = GRAM ? r : c, kk = k0 + (GRAM ? c : r);   /* short, long coordinate */
+    row = TALL ? kk : i;
+    col = TALL ? i : kk;
+    const int64_t left = row < s.rows ? s.cols - col : 0;
+    cnt = left >= 4 ? 4 : (left > 0 ? static_cast<int>(left) : 0);
+}
+
+template <bool BF16, bool TALL, bool GRAM, int LROW, int LCOL>
+__device__ __forceinline__ void fetch(const GramArgs& a, int64_t z, int64_t k0, Raw& x)
+{
     const OrthoSrc& s = a.s;
-    f32x4_t mom[8];
-    int64_t row[8], col[8];
-    int cnt[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        int r, c;
-        Sh::run(j, r, c);
-        const int64_t i = GRAM ? r : c, kk = k0 + (GRAM ? c : r);   /* short, long coordinate */
-        row[j] = TALL ? kk : i;
-        col[j] = TALL ? i : kk;
-        const int64_t left = row[j] < s.rows ? s.cols - col[j] : 0;
-        cnt[j] = left >= 4 ? 4 : (left > 0 ? static_cast<int>(left) : 0);
+        int64_t row, col;
+        int cnt;
+        place<TALL, GRAM, LROW, LCOL>(s, k0, j, row, col, cnt);
+        x.g[j] = grad4<BF16>(s, z * s.gbs + row * s.grs + col, cnt, a.g_vec);
+        if (s.M != nullptr)
+            x.m[j] = momentum4(s, z * s.mbs + row * s.mrs + col, cnt, a.m_vec);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        v[j] = grad4<BF16>(s, z * s.gbs + row[j] * s.grs + col[j], cnt[j], a.g_vec);
-    if (s.M != nullptr) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            mom[j] = momentum4(s, z * s.mbs + row[j] * s.mrs + col[j], cnt[j], a.m_vec);
-    }
+}
+
+/* g~ of a fetched share in x.g.  The first pass (GRAM) updates the momentum in
+ * memory; the second reads it as it is after the update. */
+template <bool TALL, bool GRAM, int LROW, int LCOL>
+__device__ __forceinline__ void finish(const GramArgs& a, const GradVals& k, int64_t z, int64_t k0, Raw& x)
+{
+    const OrthoSrc& s = a.s;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
+        int64_t row, col;
+        int cnt;
+        place<TALL, GRAM, LROW, LCOL>(s, k0, j, row, col, cnt);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            float g = v[j][e] * k.inv_scale;
+            float g = x.g[j][e] * k.inv_scale;
             if (k.clip)
                 g = g * k.C;
-            v[j][e] = g;
+            x.g[j][e] = g;
         }
         if (s.M != nullptr) {
             if constexpr (GRAM) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    mom[j][e] = s.sc.form == HPO_MUON_MOMENTUM_SUM ? s.sc.mu * mom[j][e] + v[j][e]
-                                                                    : s.sc.mu * mom[j][e] + s.sc.omu * v[j][e];
-                float* M = s.M + z * s.mbs + row[j] * s.mrs + col[j];
-                if (a.m_vec && cnt[j] >= 4) {
-                    *reinterpret_cast<f32x4_t*>(M) = mom[j];
+                    x.m[j][e] = s.sc.form == HPO_MUON_MOMENTUM_SUM ? s.sc.mu * x.m[j][e] + x.g[j][e]
+                                                                    : s.sc.mu * x.m[j][e] + s.sc.omu * x.g[j][e];
+                float* M = s.M + z * s.mbs + row * s.mrs + col;
+                if (a.m_vec && cnt >= 4) {
+                    *reinterpret_cast<f32x4_t*>(M) = x.m[j];
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (e < cnt[j])
-                            M[e] = mom[j][e];
+                        if (e < cnt)
+                            M[e] = x.m[j][e];
                 }
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                v[j][e] = nesterov_of(v[j][e], mom[j][e], s.sc);
+                x.g[j][e] = nesterov_of(x.g[j][e], x.m[j][e], s.sc);
         }
-        /* 0 * inv_scale is 0 or, behind the edge of a NaN clip, not a number: edges are zeros */
+        /* behind the edge 0 * C is 0 or, with a clip that is not a number, not one: edges are zeros */
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (e >= cnt[j])
-                v[j][e] = 0.0f;
+            if (e >= cnt)
+                x.g[j][e] = 0.0f;
     }
 }
 
-/* h and LO * l of eight values x * 2^e as 16-byte pieces. */
+/* h and LO * l of two values as packed pairs, both rounded to nearest even: l is
+ * as often of the other sign as h, so the dropped l l does not add up. */
+template <int LO>
+__device__ __forceinline__ void split2(float a, float b, uint32_t& h, uint32_t& l)
+{
+    const f32x2_t x = {a, b};
+    const f16x2_t hv = __builtin_convertvector(x, f16x2_t);
+    const f32x2_t r = {static_cast<float>(LO) * (a - static_cast<float>(hv[0])),
+                       static_cast<float>(LO) * (b - static_cast<float>(hv[1]))};
+    h = __builtin_bit_cast(uint32_t, hv);
+    l = __builtin_bit_cast(uint32_t, __builtin_convertvector(r, f16x2_t));
+}
+
 template <int LO>
 __device__ __forceinline__ void split8(const float (&y)[8], u32x4_t& h, u32x4_t& l)
 {
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
-        uint32_t hb[2], lb[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float x = y[2 * w + e];
-            hb[e] = f16_bits(x);
-            lb[e] = f16_bits(static_cast<float>(LO) * (x - f16v(static_cast<uint16_t>(hb[e]))));
-        }
-        h[w] = hb[0] | (hb[1] << 16);
-        l[w] = lb[0] | (lb[1] << 16);
+        uint32_t hb, lb;
+        split2<LO>(y[2 * w], y[2 * w + 1], hb, lb);
+        h[w] = hb;
+        l[w] = lb;
     }
+}
+
+/* Where the four values of rows 32 bi + 8 q + 4 (lane / 32) .. + 3, column 32 bj +
+ * lane % 32 of a partial S lie, in units of four. */
+template <int MP>
+__device__ __forceinline__ int part_at(int bi, int bj, int q, int lane)
+{
+    return ((bi * (MP / 32) + bj) * 4 + q) * 64 + lane;
 }
 
 /* ---------------------------------------------------------------------- */
@@ -281,9 +313,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram(GramArgs a)
             acc[i][j] = f32x16_t{};
     int top = -1000;   /* the sums are scaled by 2^(2 (kTop - top)) */
     using Sh = Share<MP, KC, !TALL>;
+    Raw x;
+    fetch<BF16, TALL, true, MP, KC>(a, z, c0, x);
     for (int64_t k0 = c0; k0 < c1; k0 += KC) {
-        f32x4_t v[8];
-        load_share<BF16, TALL, true, MP, KC>(a, gv, z, k0, v);
+        finish<TALL, true, MP, KC>(a, gv, z, k0, x);
+        const f32x4_t(&v)[8] = x.g;
         uint32_t m = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -328,8 +362,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram(GramArgs a)
         for (int q = 0; q < 4; ++q) {
             float y[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-                y[x] = __builtin_ldexpf(Sh::at(v, q, x), up);
+            for (int t = 0; t < 8; ++t)
+                y[t] = __builtin_ldexpf(Sh::at(v, q, t), up);
             u32x4_t h, l;
             split8<2>(y, h, l);
             int r, c;
@@ -339,6 +373,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram(GramArgs a)
             *reinterpret_cast<u32x4_t*>(lds + kBytes + off) = l;
         }
         __syncthreads();
+        if (k0 + KC < c1)   /* the next tile arrives under this one's products */
+            fetch<BF16, TALL, true, MP, KC>(a, z, k0 + KC, x);
 #pragma unroll
         for (int s = 0; s < kSlices; ++s) {
             u32x4_t fa[kB], fb[kB], fl[kB];
@@ -360,6 +396,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram(GramArgs a)
     float* out = a.part + (z * a.chunks + blockIdx.x) * (MP * MP);
     if (tid == 0)
         a.part_exp[z * a.chunks + blockIdx.x] = top;
+    /* in the order of the registers that the next kernel sums them in: four rows of one column
+     * a lane, 1 KB an access */
     if constexpr (kSplitK) {
         /* the four wavefronts' quarters, in order */
         float* buf = reinterpret_cast<float*>(lds);
@@ -368,48 +406,67 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram(GramArgs a)
         for (int r = 0; r < 16; ++r)
             buf[(wave * 16 + r) * 64 + lane] = acc[0][0][r];
         __syncthreads();
+        f32x4_t t;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int r = wave * 4 + x;
-            const float t = ((buf[r * 64 + lane] + buf[(16 + r) * 64 + lane]) + buf[(32 + r) * 64 + lane]) +
-                            buf[(48 + r) * 64 + lane];
-            out[(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * MP + (lane & 31)] = t;
+        for (int e = 0; e < 4; ++e) {
+            const int r = wave * 4 + e;
+            t[e] = ((buf[r * 64 + lane] + buf[(16 + r) * 64 + lane]) + buf[(32 + r) * 64 + lane]) +
+                   buf[(48 + r) * 64 + lane];
         }
+        reinterpret_cast<f32x4_t*>(out)[part_at<MP>(0, 0, wave, lane)] = t;
     } else {
 #pragma unroll
         for (int i = 0; i < kB; ++i)
 #pragma unroll
             for (int j = 0; j < kB; ++j)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    out[(r0 + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) * MP + q0 + 32 * j + (lane & 31)] =
-                        acc[i][j][r];
+                for (int q = 0; q < 4; ++q) {
+                    f32x4_t t;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        t[e] = acc[i][j][4 * q + e];
+                    reinterpret_cast<f32x4_t*>(out)[part_at<MP>(r0 / 32 + i, q0 / 32 + j, q, lane)] = t;
+                }
     }
 }
 
 /* ---------------------------------------------------------------------- */
 /* the steps in the m x m space                                            */
 /* ---------------------------------------------------------------------- */
-/* One workgroup per matrix (grid: batch), W x W wavefronts of B x B blocks.
+/* One workgroup per matrix (grid: batch), WM x WN wavefronts of BM x BN blocks.
  * All operands are symmetric, so a matrix in LDS (rows of MP, h then l) serves
  * as left and as right operand, and a lane's four consecutive rows of one
- * column are stored as four consecutive columns of one row. */
+ * column are stored as four consecutive columns of one row: mul(x, y) is x^T y.
+ * A is formed as Q^T A Q, from both sides: where roundings leave A and Q not quite symmetric,
+ * a one-sided A^T Q Q grows that part by Q^2 a step (2 x 2 with singular values 1 and 0.02:
+ * 6e-2 off after five).  Products stay at the
+ * scale of their operands' exponents; the next split or sum takes that in (an
+ * exact power of two). */
 template <int MP>
-__global__ __launch_bounds__(MP == 32 ? 64 : 256) void k_gram_iterate(GramArgs a)
+struct Iter {
+    static constexpr int WM = MP / 32, WN = MP == 32 ? 1 : 2;
+    static constexpr int BN = MP / 32 / WN;   /* blocks of a wavefront: one row, BN columns */
+    static constexpr int kThreads = 64 * WM * WN;
+};
+
+__device__ __forceinline__ float pow2f(int e) { return __builtin_ldexpf(1.0f, e); }
+
+template <int MP>
+__global__ __launch_bounds__(Iter<MP>::kThreads) void k_gram_iterate(GramArgs a)
 {
     if (!gate_open(a.s.sc.gate))
         return;
-    constexpr int W = MP == 32 ? 1 : 2, B = MP / 32 / W;
-    constexpr int NT = 64 * W * W;
+    constexpr int WN = Iter<MP>::WN, BN = Iter<MP>::BN;
     constexpr int kPlane = MP * MP * 2, kBuf = 2 * kPlane;
     constexpr int kRaw = MP * (MP + 1) * 4;
     __shared__ __attribute__((aligned(16))) char lds[2 * kBuf > kRaw ? 2 * kBuf : kRaw];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-    const int r0 = (wave / W) * 32 * B, q0 = (wave % W) * 32 * B;
+    const int r0 = (wave / WN) * 32, q0 = (wave % WN) * 32 * BN;
     const int64_t z = blockIdx.x;
-    typedef f32x16_t Block[B][B];
-    auto row_of = [&](int i, int r) { return r0 + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3); };
-    auto col_of = [&](int j) { return q0 + 32 * j + (lane & 31); };
+    typedef f32x16_t Block[BN];
+    const int lrow = r0 + 4 * (lane >> 5), lcol = q0 + (lane & 31);
+    auto row_of = [&](int r) { return lrow + 8 * (r >> 2) + (r & 3); };
+    auto col_of = [&](int j) { return lcol + 32 * j; };
 
     /* S: the parts at their largest exponent, in order */
     const int32_t* pe = a.part_exp + z * a.chunks;
@@ -418,38 +475,37 @@ __global__ __launch_bounds__(MP == 32 ? 64 : 256) void k_gram_iterate(GramArgs a
         top = pe[c] > top ? pe[c] : top;
     Block A, P, Q, acc;
 #pragma unroll
-    for (int i = 0; i < B; ++i)
-#pragma unroll
-        for (int j = 0; j < B; ++j)
-            A[i][j] = f32x16_t{};
+    for (int j = 0; j < BN; ++j)
+        A[j] = f32x16_t{};
+#pragma unroll 2
     for (int c = 0; c < a.chunks; ++c) {
-        const float* part = a.part + (z * a.chunks + c) * (MP * MP);
+        const f32x4_t* part = reinterpret_cast<const f32x4_t*>(a.part + (z * a.chunks + c) * (MP * MP));
         const int d = 2 * (pe[c] - top);
+        f32x4_t t[BN][4];
 #pragma unroll
-        for (int i = 0; i < B; ++i)
+        for (int j = 0; j < BN; ++j)
 #pragma unroll
-            for (int j = 0; j < B; ++j)
+            for (int q = 0; q < 4; ++q)
+                t[j][q] = part[part_at<MP>(r0 / 32, q0 / 32 + j, q, lane)];
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    A[i][j][r] += __builtin_ldexpf(part[row_of(i, r) * MP + col_of(j)], d);
+        for (int j = 0; j < BN; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                A[j][r] += __builtin_ldexpf(t[j][r >> 2][r & 3], d);
     }
     /* (S + S^T) / 2 and the trace */
     float* raw = reinterpret_cast<float*>(lds);
 #pragma unroll
-    for (int i = 0; i < B; ++i)
+    for (int j = 0; j < BN; ++j)
 #pragma unroll
-        for (int j = 0; j < B; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                raw[row_of(i, r) * (MP + 1) + col_of(j)] = A[i][j][r];
+        for (int r = 0; r < 16; ++r)
+            raw[row_of(r) * (MP + 1) + col_of(j)] = A[j][r];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < B; ++i)
+    for (int j = 0; j < BN; ++j)
 #pragma unroll
-        for (int j = 0; j < B; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                A[i][j][r] = 0.5f * (A[i][j][r] + raw[col_of(j) * (MP + 1) + row_of(i, r)]);
+        for (int r = 0; r < 16; ++r)
+            A[j][r] = 0.5f * (A[j][r] + raw[col_of(j) * (MP + 1) + row_of(r)]);
     /* every lane of every wavefront sums the same diagonal in the same order */
     double trace = 0.0;
     for (int i = lane; i < MP; i += 64)
@@ -471,135 +527,118 @@ __global__ __launch_bounds__(MP == 32 ? 64 : 256) void k_gram_iterate(GramArgs a
         a.inv[2 * z + 1] = static_cast<float>(e + kTop);
     }
 #pragma unroll
-    for (int i = 0; i < B; ++i)
+    for (int j = 0; j < BN; ++j)
 #pragma unroll
-        for (int j = 0; j < B; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                A[i][j][r] = static_cast<float>(static_cast<double>(A[i][j][r]) * f);
+        for (int r = 0; r < 16; ++r)
+            A[j][r] = static_cast<float>(static_cast<double>(A[j][r]) * f);
 
     char* b0 = lds;
     char* b1 = lds + kBuf;
+    /* x * 2^e, split, into buf */
     auto put = [&](char* buf, const Block& x, int e) {
+        const float s = pow2f(e);
 #pragma unroll
-        for (int i = 0; i < B; ++i)
+        for (int j = 0; j < BN; ++j)
 #pragma unroll
-            for (int j = 0; j < B; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    /* rows row_of(i, 4 q) + 0..3 of column col_of(j), stored as that row's columns */
-                    uint32_t h[4], l[4];
-#pragma unroll
-                    for (int x4 = 0; x4 < 4; ++x4) {
-                        const float y = __builtin_ldexpf(x[i][j][4 * q + x4], e);
-                        h[x4] = f16_bits(y);
-                        l[x4] = f16_bits(y - f16v(static_cast<uint16_t>(h[x4])));
-                    }
-                    const int c = row_of(i, 4 * q);
-                    const int off = piece_at<MP>(col_of(j), c >> 3) + ((c >> 2) & 1) * 8;
-                    u32x2_t t;
-                    t.x = h[0] | (h[1] << 16);
-                    t.y = h[2] | (h[3] << 16);
-                    *reinterpret_cast<u32x2_t*>(buf + off) = t;
-                    t.x = l[0] | (l[1] << 16);
-                    t.y = l[2] | (l[3] << 16);
-                    *reinterpret_cast<u32x2_t*>(buf + kPlane + off) = t;
-                }
+            for (int q = 0; q < 4; ++q) {
+                /* rows row_of(4 q) + 0..3 of column col_of(j), stored as that row's columns */
+                u32x2_t h, l;
+                uint32_t hb, lb;
+                split2<1>(x[j][4 * q] * s, x[j][4 * q + 1] * s, hb, lb);
+                h.x = hb;
+                l.x = lb;
+                split2<1>(x[j][4 * q + 2] * s, x[j][4 * q + 3] * s, hb, lb);
+                h.y = hb;
+                l.y = lb;
+                const int c = lrow + 8 * q;
+                const int off = piece_at<MP>(col_of(j), c >> 3) + ((c >> 2) & 1) * 8;
+                *reinterpret_cast<u32x2_t*>(buf + off) = h;
+                *reinterpret_cast<u32x2_t*>(buf + kPlane + off) = l;
+            }
     };
-    /* acc = x y * 2^-e */
-    auto mul = [&](const char* x, const char* y, Block& out, int e) {
+    auto mul = [&](const char* x, const char* y, Block& out) {
 #pragma unroll
-        for (int i = 0; i < B; ++i)
-#pragma unroll
-            for (int j = 0; j < B; ++j)
-                out[i][j] = f32x16_t{};
+        for (int j = 0; j < BN; ++j)
+            out[j] = f32x16_t{};
 #pragma unroll
         for (int s = 0; s < MP / 16; ++s) {
-            u32x4_t xh[B], xl[B], yh[B], yl[B];
+            u32x4_t yh[BN], yl[BN];
+            const u32x4_t xh = fragment<MP>(x, r0, s), xl = fragment<MP>(x + kPlane, r0, s);
 #pragma unroll
-            for (int i = 0; i < B; ++i) {
-                xh[i] = fragment<MP>(x, r0 + 32 * i, s);
-                xl[i] = fragment<MP>(x + kPlane, r0 + 32 * i, s);
-                yh[i] = fragment<MP>(y, q0 + 32 * i, s);
-                yl[i] = fragment<MP>(y + kPlane, q0 + 32 * i, s);
+            for (int j = 0; j < BN; ++j) {
+                yh[j] = fragment<MP>(y, q0 + 32 * j, s);
+                yl[j] = fragment<MP>(y + kPlane, q0 + 32 * j, s);
             }
 #pragma unroll
-            for (int i = 0; i < B; ++i)
+            for (int j = 0; j < BN; ++j)
+                out[j] = mfma(xh, yh[j], out[j]);
 #pragma unroll
-                for (int j = 0; j < B; ++j) {
-                    out[i][j] = mfma(xh[i], yh[j], out[i][j]);
-                    out[i][j] = mfma(xh[i], yl[j], out[i][j]);
-                    out[i][j] = mfma(xl[i], yh[j], out[i][j]);
-                }
+            for (int j = 0; j < BN; ++j)
+                out[j] = mfma(xh, yl[j], out[j]);
+#pragma unroll
+            for (int j = 0; j < BN; ++j)
+                out[j] = mfma(xl, yh[j], out[j]);
         }
-#pragma unroll
-        for (int i = 0; i < B; ++i)
-#pragma unroll
-            for (int j = 0; j < B; ++j)
-#pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    out[i][j][r] = __builtin_ldexpf(out[i][j][r], -e);
     };
 
+    int ae = 0, pq = 0;   /* A's and P's registers hold A 2^ae and P 2^pq */
     put(b0, A, a.step[0].a_exp);
     __syncthreads();
     for (int k = 0; k < a.steps; ++k) {
         const GramStep& g = a.step[k];
         const bool first = k == 0, last = k + 1 == a.steps;
-        mul(b0, b0, acc, 2 * g.a_exp);
+        mul(b0, b0, acc);
+        const float fb = g.b * pow2f(-ae), fc = g.c * pow2f(-2 * g.a_exp);
 #pragma unroll
-        for (int i = 0; i < B; ++i)
+        for (int j = 0; j < BN; ++j)
 #pragma unroll
-            for (int j = 0; j < B; ++j)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const float q = g.b * A[i][j][r] + g.c * acc[i][j][r];
-                    Q[i][j][r] = row_of(i, r) == col_of(j) ? g.a + q : q;
-                }
+            for (int r = 0; r < 16; ++r) {
+                const float diag = row_of(r) == col_of(j) ? g.a : 0.0f;
+                Q[j][r] = diag + (fb * A[j][r] + fc * acc[j][r]);
+            }
         if (first) {
 #pragma unroll
-            for (int i = 0; i < B; ++i)
-#pragma unroll
-                for (int j = 0; j < B; ++j)
-                    P[i][j] = Q[i][j];
+            for (int j = 0; j < BN; ++j)
+                P[j] = Q[j];
         }
         if (first && last)
             break;
         put(b1, Q, g.q_exp);
         __syncthreads();
         if (!last)
-            mul(b1, b0, acc, g.q_exp + g.a_exp);   /* T = Q A */
+            mul(b0, b1, acc);   /* T = A^T Q */
         if (!first) {
             __syncthreads();
-            put(b0, P, g.p_exp);
+            put(b0, P, g.p_exp - pq);
             __syncthreads();
-            mul(b1, b0, P, g.q_exp + g.p_exp);
+            mul(b1, b0, P);
+            pq = g.q_exp + g.p_exp;
         }
         if (!last) {
             __syncthreads();
-            put(b0, acc, g.t_exp);
+            put(b0, acc, g.t_exp - g.q_exp - g.a_exp);
             __syncthreads();
-            mul(b0, b1, A, g.t_exp + g.q_exp);     /* A = T Q */
+            mul(b0, b1, A);     /* A = T^T Q = Q^T A Q */
+            ae = g.t_exp + g.q_exp;
             __syncthreads();
-            put(b0, A, a.step[k + 1].a_exp);
+            put(b0, A, a.step[k + 1].a_exp - ae);
             __syncthreads();
         }
     }
-    /* P for the last pass: rows of 16-bit values, h then l */
+    /* P for the last pass: rows of 16-bit values, h then l (P is symmetric) */
     uint16_t* out = a.P + z * (2 * MP * MP);
+    const float s = pow2f(a.p_exp - pq);
 #pragma unroll
-    for (int i = 0; i < B; ++i)
+    for (int j = 0; j < BN; ++j)
 #pragma unroll
-        for (int j = 0; j < B; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float y = __builtin_ldexpf(P[i][j][r], a.p_exp);
-                const uint32_t h = f16_bits(y);
-                const int at = row_of(i, r) * MP + col_of(j);
-                out[at] = static_cast<uint16_t>(h);
-                out[MP * MP + at] = static_cast<uint16_t>(f16_bits(y - f16v(static_cast<uint16_t>(h))));
-            }
-    (void)NT;
+        for (int q = 0; q < 4; ++q) {
+            uint32_t h0, h1, l0, l1;
+            split2<1>(P[j][4 * q] * s, P[j][4 * q + 1] * s, h0, l0);
+            split2<1>(P[j][4 * q + 2] * s, P[j][4 * q + 3] * s, h1, l1);
+            const int at = col_of(j) * MP + lrow + 8 * q;
+            *reinterpret_cast<u32x2_t*>(out + at) = u32x2_t{h0, h1};
+            *reinterpret_cast<u32x2_t*>(out + MP * MP + at) = u32x2_t{l0, l1};
+        }
 }
 
 /* ---------------------------------------------------------------------- */
@@ -622,8 +661,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram_apply(GramArgs a)
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const GradVals gv = grad_vals(a.s.sc);
     const int64_t z = blockIdx.y;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.run;
-    const int64_t c1 = c0 + a.run < a.n ? c0 + a.run : a.n;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.apply_run;
+    const int64_t c1 = c0 + a.apply_run < a.n ? c0 + a.apply_run : a.n;
     const float mant = a.inv[2 * z];
     const int ex = static_cast<int>(a.inv[2 * z + 1]);
     const int i0 = (wave % kRowBlocks) * 32, j0 = (wave / kRowBlocks) * 64;
@@ -636,19 +675,18 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram_apply(GramArgs a)
         pl[s] = *reinterpret_cast<const u32x4_t*>(P + MP * MP + at);
     }
     using Sh = Share<KC, MP, TALL>;
+    Raw x;
+    fetch<BF16, TALL, false, KC, MP>(a, z, c0, x);
     for (int64_t k0 = c0; k0 < c1; k0 += KC) {
-        f32x4_t v[8];
-        load_share<BF16, TALL, false, KC, MP>(a, gv, z, k0, v);
+        finish<TALL, false, KC, MP>(a, gv, z, k0, x);
+        const f32x4_t(&v)[8] = x.g;
         __syncthreads();   /* the previous tile's fragments are read */
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             float y[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const float g = Sh::at(v, q, x);
-                /* a stack of zeros with eps = 0 stays 0 */
-                y[x] = __builtin_ldexpf(g * mant, ex);
-            }
+            for (int t = 0; t < 8; ++t)
+                y[t] = __builtin_ldexpf(Sh::at(v, q, t) * mant, ex);
             u32x4_t h, l;
             split8<1>(y, h, l);
             int r, c;
@@ -658,6 +696,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram_apply(GramArgs a)
             *reinterpret_cast<u32x4_t*>(lds + kBytes + off) = l;
         }
         __syncthreads();
+        if (k0 + KC < c1)
+            fetch<BF16, TALL, false, KC, MP>(a, z, k0 + KC, x);
         f32x16_t acc[2] = {f32x16_t{}, f32x16_t{}};
 #pragma unroll
         for (int s = 0; s < kSlices; ++s) {
@@ -702,7 +742,7 @@ int mp_of(int64_t m) { return m <= 32 ? 32 : (m <= 64 ? 64 : 128); }
 
 struct GramPlan {
     int mp;
-    int64_t m, n, run, chunks, count;
+    int64_t m, n, run, apply_run, chunks, count;
     int64_t slot;   /* bytes of one matrix */
 };
 
@@ -722,6 +762,10 @@ GramPlan gram_plan(int64_t batch, int64_t rows, int64_t cols)
     per = (tiles + p.chunks - 1) / p.chunks;
     p.chunks = (tiles + per - 1) / per;
     p.run = per * kc;
+    /* the last pass has no partial results: three workgroups a CU, two tiles each at the least */
+    int64_t last = (tiles * batch + 767) / 768;
+    last = last < 2 ? 2 : last;
+    p.apply_run = last * kc;
     p.slot = (4 * p.chunks + 4) * p.mp * p.mp + 4 * p.chunks + 8;
     constexpr int64_t kCap = int64_t{4} << 30;
     const int64_t most = kCap / p.slot > 1 ? kCap / p.slot : 1;
@@ -737,10 +781,11 @@ hipError_t run(const GramArgs& a, uint32_t count, hipStream_t stream)
     hipError_t e = launch(k_gram<BF16, MP, TALL>, grid, kThreads, stream, a);
     if (e != hipSuccess)
         return e;
-    e = launch(k_gram_iterate<MP>, dim3(count), MP == 32 ? 64 : 256, stream, a);
+    e = launch(k_gram_iterate<MP>, dim3(count), Iter<MP>::kThreads, stream, a);
     if (e != hipSuccess)
         return e;
-    return launch(k_gram_apply<BF16, MP, TALL>, grid, kThreads, stream, a);
+    const dim3 last(static_cast<uint32_t>((a.n + a.apply_run - 1) / a.apply_run), count);
+    return launch(k_gram_apply<BF16, MP, TALL>, last, kThreads, stream, a);
 }
 
 template <bool BF16, int MP>
@@ -778,6 +823,7 @@ hipError_t launch_gram(const OrthoArgs& o, hipStream_t stream)
         a.m = p.m;
         a.n = p.n;
         a.run = p.run;
+        a.apply_run = p.apply_run;
         a.chunks = static_cast<int32_t>(p.chunks);
         a.g_vec = o.g_vec;
         a.m_vec = o.m_vec;

@@ -55,6 +55,8 @@
  */
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "hpo_muon_device.h"
@@ -1435,15 +1437,42 @@ struct OrthoPlan {
 
 int64_t pad_to(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 
+/* Time of one step's three products (us) with a tile of side t: every launch
+ * costs `fixed`, and a k of the products `alone` while the grid is resident at once, `full` a
+ * workgroup per CU beyond.  Fitted to 19 shapes from 256 x 256 to 4096 x 4096 in stacks of
+ * 1 to 64 on each tile, five steps each: 1 x 1024 x 1024 takes 461 / 283 / 164 us with
+ * 256 / 128 / 64, 2 x 2048 x 2048 739 / 578 / 782, 1 x 4096 x 4096 1624 / 1856 / 2788. */
+double step_us(int64_t batch, int64_t m, int64_t n, int64_t t)
+{
+    constexpr double kCus = 256.0;
+    const double mt = static_cast<double>(pad_to(m, t) / t), nt = static_cast<double>(pad_to(n, t) / t);
+    const double b = static_cast<double>(batch), k = static_cast<double>(t);
+    auto launch_us = [&](double wgs, double depth, bool general) {
+        if (t == GenTile::kBM)   /* one workgroup a CU: the general product's stores are not overlapped */
+            return 12.5 + (general ? 20.0 * std::min(1.0, wgs / kCus) : 0.0) + 0.0167 * depth * std::ceil(wgs / kCus);
+        if (t == MidTile::kBM)
+            return 7.0 + depth * (wgs <= kCus ? 0.0102 : 0.0085 * std::ceil(wgs / kCus));
+        return 3.2 + depth * (wgs <= 2 * kCus ? 0.0062 : 0.0038 * std::ceil(wgs / kCus));
+    };
+    const double tri = b * mt * (mt + 1.0) / 2.0;
+    return launch_us(tri, k * nt, false) + launch_us(tri, k * mt, false) + launch_us(b * mt * nt, k * mt, true);
+}
+
+int32_t pick_tile(int64_t batch, int64_t m, int64_t n)
+{
+    int32_t best = GenTile::kBM;
+    for (int32_t t : {static_cast<int32_t>(MidTile::kBM), static_cast<int32_t>(SmallTile::kBM)})
+        if (step_us(batch, m, n, t) < step_us(batch, m, n, best))
+            best = t;
+    return best;
+}
+
 OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols)
 {
     OrthoPlan p{};
     p.m = rows > cols ? cols : rows;
     p.n = rows > cols ? rows : cols;
-    /* the largest tile whose grid (of the step's product) still gives every CU a workgroup */
-    auto grid = [&](int64_t t) { return batch * (pad_to(p.m, t) / t) * (pad_to(p.n, t) / t); };
-    constexpr int64_t kCus = 256;
-    p.tile = grid(GenTile::kBM) >= kCus ? GenTile::kBM : (grid(MidTile::kBM) >= kCus ? MidTile::kBM : SmallTile::kBM);
+    p.tile = pick_tile(batch, p.m, p.n);
     p.mp = pad_to(p.m, p.tile);
     p.np = pad_to(p.n, p.tile);
     p.parts = sum_parts(rows, cols);

@@ -90,7 +90,7 @@ def check_ortho(got, g64, steps=5, coeffs=None, eps=1e-7, tag=""):
         assert d <= tol * n, (tag, z, d, n)
 
 
-@pytest.mark.parametrize("b,r,c", [(1, 1, 1), (1, 1, 300), (2, 300, 1), (3, 2, 7), (2, 64, 64), (2, 128, 640),
+@pytest.mark.parametrize("b,r,c", [(1, 1, 1), (1, 1, 300), (2, 300, 1), (3, 2, 7), (2, 2, 2), (2, 16, 16), (2, 64, 64), (2, 128, 640),
                                    (2, 640, 128), (3, 129, 257), (1, 256, 256), (2, 300, 520), (1, 520, 300),
                                    (5, 33, 1000), (4, 128, 129), (2, 96, 2048), (1, 17, 16384)])
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
