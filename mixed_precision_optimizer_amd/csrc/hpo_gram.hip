@@ -28,6 +28,8 @@
  */
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "hpo_muon_device.h"
 
 namespace hpo {
@@ -40,6 +42,9 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+/* four elements at any element's address (one instruction in global memory) */
+typedef f32x4_t f32x4_any __attribute__((aligned(4)));
+typedef u32x2_t u32x2_any __attribute__((aligned(2)));
 
 constexpr int kThreads = 256;
 constexpr int kTileElems = 8192;   /* elements of a column tile: 32 per thread */
@@ -48,12 +53,9 @@ constexpr int kTop = 14;           /* values are scaled to at most 2^14 */
 struct GramArgs {
     OrthoSrc s;
     int64_t m, n;        /* short and long side */
-    int64_t run;         /* columns (of the wide form) a workgroup takes, whole tiles */
-    int64_t apply_run;   /* the same for the last pass */
-    int32_t chunks;      /* workgroups per matrix of the first */
-    int32_t g_vec;       /* rows of G, M and out take 4-element accesses */
-    int32_t m_vec;
-    int32_t o_vec;
+    int64_t run;         /* columns (of the wide form) a workgroup takes in either pass, whole tiles */
+    int32_t chunks;      /* workgroups per matrix */
+    int32_t summed;      /* k_gram_sum has added the parts up */
     float* part;         /* [batch][chunks][MP][MP] */
     int32_t* part_exp;   /* [batch][chunks] */
     uint16_t* P;         /* [batch][2][MP][MP]: h and l of P * 2^p_exp */
@@ -95,18 +97,18 @@ __device__ __forceinline__ u32x4_t fragment(const char* base, int row0, int slic
 
 /* Four consecutive stored elements: n of them are there (the others read as 0). */
 template <bool BF16>
-__device__ __forceinline__ f32x4_t grad4(const OrthoSrc& s, int64_t at, int n, bool vec)
+__device__ __forceinline__ f32x4_t grad4(const OrthoSrc& s, int64_t at, int n)
 {
     f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (vec && n >= 4) {
+    if (n >= 4) {
         if constexpr (BF16) {
-            const u32x2_t t = *reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(s.G) + at);
+            const u32x2_t t = *reinterpret_cast<const u32x2_any*>(static_cast<const uint16_t*>(s.G) + at);
             x[0] = bf16_to_f32(t.x & 0xffffu);
             x[1] = bf16_to_f32(t.x >> 16);
             x[2] = bf16_to_f32(t.y & 0xffffu);
             x[3] = bf16_to_f32(t.y >> 16);
         } else {
-            x = *reinterpret_cast<const f32x4_t*>(static_cast<const float*>(s.G) + at);
+            x = *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(s.G) + at);
         }
         return x;
     }
@@ -117,11 +119,11 @@ __device__ __forceinline__ f32x4_t grad4(const OrthoSrc& s, int64_t at, int n, b
     return x;
 }
 
-__device__ __forceinline__ f32x4_t momentum4(const OrthoSrc& s, int64_t at, int n, bool vec)
+__device__ __forceinline__ f32x4_t momentum4(const OrthoSrc& s, int64_t at, int n)
 {
     f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (vec && n >= 4)
-        return *reinterpret_cast<const f32x4_t*>(s.M + at);
+    if (n >= 4)
+        return *reinterpret_cast<const f32x4_any*>(s.M + at);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
         if (e < n)
@@ -195,9 +197,9 @@ __device__ __forceinline__ void fetch(const GramArgs& a, int64_t z, int64_t k0, 
         int64_t row, col;
         int cnt;
         place<TALL, GRAM, LROW, LCOL>(s, k0, j, row, col, cnt);
-        x.g[j] = grad4<BF16>(s, z * s.gbs + row * s.grs + col, cnt, a.g_vec);
+        x.g[j] = grad4<BF16>(s, z * s.gbs + row * s.grs + col, cnt);
         if (s.M != nullptr)
-            x.m[j] = momentum4(s, z * s.mbs + row * s.mrs + col, cnt, a.m_vec);
+            x.m[j] = momentum4(s, z * s.mbs + row * s.mrs + col, cnt);
     }
 }
 
@@ -226,8 +228,8 @@ __device__ __forceinline__ void finish(const GramArgs& a, const GradVals& k, int
                     x.m[j][e] = s.sc.form == HPO_MUON_MOMENTUM_SUM ? s.sc.mu * x.m[j][e] + x.g[j][e]
                                                                     : s.sc.mu * x.m[j][e] + s.sc.omu * x.g[j][e];
                 float* M = s.M + z * s.mbs + row * s.mrs + col;
-                if (a.m_vec && cnt >= 4) {
-                    *reinterpret_cast<f32x4_t*>(M) = x.m[j];
+                if (cnt >= 4) {
+                    *reinterpret_cast<f32x4_any*>(M) = x.m[j];
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
@@ -430,6 +432,32 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram(GramArgs a)
     }
 }
 
+/* Sums the parts of S where they are many: a workgroup takes 1024 of each matrix's values
+ * (grid: MP^2 / 1024, batch) and leaves the sum, at the largest part's exponent, in the
+ * first part. */
+template <int MP>
+__global__ __launch_bounds__(kThreads) void k_gram_sum(GramArgs a)
+{
+    if (!gate_open(a.s.sc.gate))
+        return;
+    const int64_t z = blockIdx.y;
+    const int32_t* pe = a.part_exp + z * a.chunks;
+    int top = -1000;
+    for (int c = 0; c < a.chunks; ++c)
+        top = pe[c] > top ? pe[c] : top;
+    f32x4_t* part = reinterpret_cast<f32x4_t*>(a.part + z * a.chunks * (MP * MP)) + blockIdx.x * kThreads + threadIdx.x;
+    f32x4_t t = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int c = 0; c < a.chunks; ++c) {
+        const f32x4_t x = part[c * (MP * MP / 4)];
+        const int d = 2 * (pe[c] - top);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            t[e] += __builtin_ldexpf(x[e], d);
+    }
+    part[0] = t;
+}
+
 /* ---------------------------------------------------------------------- */
 /* the steps in the m x m space                                            */
 /* ---------------------------------------------------------------------- */
@@ -477,10 +505,9 @@ __global__ __launch_bounds__(Iter<MP>::kThreads) void k_gram_iterate(GramArgs a)
 #pragma unroll
     for (int j = 0; j < BN; ++j)
         A[j] = f32x16_t{};
-#pragma unroll 2
-    for (int c = 0; c < a.chunks; ++c) {
+    for (int c = 0; c < (a.summed ? 1 : a.chunks); ++c) {
         const f32x4_t* part = reinterpret_cast<const f32x4_t*>(a.part + (z * a.chunks + c) * (MP * MP));
-        const int d = 2 * (pe[c] - top);
+        const int d = a.summed ? 0 : 2 * (pe[c] - top);
         f32x4_t t[BN][4];
 #pragma unroll
         for (int j = 0; j < BN; ++j)
@@ -518,7 +545,9 @@ __global__ __launch_bounds__(Iter<MP>::kThreads) void k_gram_iterate(GramArgs a)
     const double unit = ldexp(1.0, top > -1000 ? top - kTop : 0);
     const float d = static_cast<float>(sqrt(trace) * unit) + a.s.sc.eps;
     const double id = d == 0.0f ? 0.0 : 1.0 / static_cast<double>(d);
-    const double f = trace == 0.0 ? 0.0 : (unit * id) * (unit * id);
+    /* the factor of A as a value in [1/2, 1) and an exponent */
+    int fe = 0;
+    const float fm = static_cast<float>(frexp(trace == 0.0 ? 0.0 : (unit * id) * (unit * id), &fe));
     if (tid == 0) {
         /* 1 / d as mantissa and exponent: it may lie beyond fp32's range */
         int e = 0;
@@ -530,7 +559,7 @@ __global__ __launch_bounds__(Iter<MP>::kThreads) void k_gram_iterate(GramArgs a)
     for (int j = 0; j < BN; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-            A[j][r] = static_cast<float>(static_cast<double>(A[j][r]) * f);
+            A[j][r] = __builtin_ldexpf(A[j][r] * fm, fe);
 
     char* b0 = lds;
     char* b1 = lds + kBuf;
@@ -556,28 +585,38 @@ __global__ __launch_bounds__(Iter<MP>::kThreads) void k_gram_iterate(GramArgs a)
                 *reinterpret_cast<u32x2_t*>(buf + kPlane + off) = l;
             }
     };
+    /* One slice's fragments are read under the last one's products (one scheduling region per
+     * slice: left alone the compiler reads far ahead and spills). */
     auto mul = [&](const char* x, const char* y, Block& out) {
 #pragma unroll
         for (int j = 0; j < BN; ++j)
             out[j] = f32x16_t{};
-#pragma unroll
-        for (int s = 0; s < MP / 16; ++s) {
-            u32x4_t yh[BN], yl[BN];
-            const u32x4_t xh = fragment<MP>(x, r0, s), xl = fragment<MP>(x + kPlane, r0, s);
+        u32x4_t xh[2], xl[2], yh[2][BN], yl[2][BN];
+        auto read = [&](int s) {
+            xh[s & 1] = fragment<MP>(x, r0, s);
+            xl[s & 1] = fragment<MP>(x + kPlane, r0, s);
 #pragma unroll
             for (int j = 0; j < BN; ++j) {
-                yh[j] = fragment<MP>(y, q0 + 32 * j, s);
-                yl[j] = fragment<MP>(y + kPlane, q0 + 32 * j, s);
+                yh[s & 1][j] = fragment<MP>(y, q0 + 32 * j, s);
+                yl[s & 1][j] = fragment<MP>(y + kPlane, q0 + 32 * j, s);
             }
+        };
+        read(0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < MP / 16; ++s) {
+            if (s + 1 < MP / 16)
+                read(s + 1);
 #pragma unroll
             for (int j = 0; j < BN; ++j)
-                out[j] = mfma(xh, yh[j], out[j]);
+                out[j] = mfma(xh[s & 1], yh[s & 1][j], out[j]);
 #pragma unroll
             for (int j = 0; j < BN; ++j)
-                out[j] = mfma(xh, yl[j], out[j]);
+                out[j] = mfma(xh[s & 1], yl[s & 1][j], out[j]);
 #pragma unroll
             for (int j = 0; j < BN; ++j)
-                out[j] = mfma(xl, yh[j], out[j]);
+                out[j] = mfma(xl[s & 1], yh[s & 1][j], out[j]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
 
@@ -661,8 +700,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram_apply(GramArgs a)
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const GradVals gv = grad_vals(a.s.sc);
     const int64_t z = blockIdx.y;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.apply_run;
-    const int64_t c1 = c0 + a.apply_run < a.n ? c0 + a.apply_run : a.n;
+    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.run;
+    const int64_t c1 = c0 + a.run < a.n ? c0 + a.run : a.n;
     const float mant = a.inv[2 * z];
     const int ex = static_cast<int>(a.inv[2 * z + 1]);
     const int i0 = (wave % kRowBlocks) * 32, j0 = (wave / kRowBlocks) * 64;
@@ -742,7 +781,7 @@ int mp_of(int64_t m) { return m <= 32 ? 32 : (m <= 64 ? 64 : 128); }
 
 struct GramPlan {
     int mp;
-    int64_t m, n, run, apply_run, chunks, count;
+    int64_t m, n, run, chunks, count;
     int64_t slot;   /* bytes of one matrix */
 };
 
@@ -753,19 +792,12 @@ GramPlan gram_plan(int64_t batch, int64_t rows, int64_t cols)
     p.n = rows > cols ? rows : cols;
     p.mp = mp_of(p.m);
     const int64_t kc = kTileElems / p.mp, tiles = (p.n + kc - 1) / kc;
-    /* enough workgroups to fill the chip twice; a run of 4 MP columns at the least keeps
-     * the partial results under a quarter of the gradient's bytes */
-    const int64_t least = 4 * p.mp / kc > 1 ? 4 * p.mp / kc : 1;
-    int64_t per = (tiles * batch + 511) / 512;
-    per = per < least ? least : per;
+    /* both passes: one round of two workgroups a CU */
+    int64_t per = std::max<int64_t>((tiles * batch + 511) / 512, 1);
     p.chunks = (tiles + per - 1) / per;
     per = (tiles + p.chunks - 1) / p.chunks;
     p.chunks = (tiles + per - 1) / per;
     p.run = per * kc;
-    /* the last pass has no partial results: three workgroups a CU, two tiles each at the least */
-    int64_t last = (tiles * batch + 767) / 768;
-    last = last < 2 ? 2 : last;
-    p.apply_run = last * kc;
     p.slot = (4 * p.chunks + 4) * p.mp * p.mp + 4 * p.chunks + 8;
     constexpr int64_t kCap = int64_t{4} << 30;
     const int64_t most = kCap / p.slot > 1 ? kCap / p.slot : 1;
@@ -781,11 +813,15 @@ hipError_t run(const GramArgs& a, uint32_t count, hipStream_t stream)
     hipError_t e = launch(k_gram<BF16, MP, TALL>, grid, kThreads, stream, a);
     if (e != hipSuccess)
         return e;
+    if (a.summed) {
+        e = launch(k_gram_sum<MP>, dim3(MP * MP / 4 / kThreads, count), kThreads, stream, a);
+        if (e != hipSuccess)
+            return e;
+    }
     e = launch(k_gram_iterate<MP>, dim3(count), Iter<MP>::kThreads, stream, a);
     if (e != hipSuccess)
         return e;
-    const dim3 last(static_cast<uint32_t>((a.n + a.apply_run - 1) / a.apply_run), count);
-    return launch(k_gram_apply<BF16, MP, TALL>, last, kThreads, stream, a);
+    return launch(k_gram_apply<BF16, MP, TALL>, grid, kThreads, stream, a);
 }
 
 template <bool BF16, int MP>
@@ -823,10 +859,9 @@ hipError_t launch_gram(const OrthoArgs& o, hipStream_t stream)
         a.m = p.m;
         a.n = p.n;
         a.run = p.run;
-        a.apply_run = p.apply_run;
         a.chunks = static_cast<int32_t>(p.chunks);
-        a.g_vec = o.g_vec;
-        a.m_vec = o.m_vec;
+        /* one workgroup reads about 256 KB in the time that another launch costs */
+        a.summed = p.chunks * p.mp * p.mp * 4 > (int64_t{1} << 18) ? 1 : 0;
         char* at = static_cast<char*>(o.ws);
         a.part = reinterpret_cast<float*>(at);
         at += 4 * p.count * p.chunks * p.mp * p.mp;

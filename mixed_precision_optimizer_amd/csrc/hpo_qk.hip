@@ -30,6 +30,8 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+/* eight elements at any element's address (one instruction in global memory) */
+typedef u32x4_t u32x4_any __attribute__((aligned(2)));
 
 constexpr int kQkThreads = 256;
 constexpr int kQkWaves = 4;
@@ -72,17 +74,30 @@ __device__ __forceinline__ void buffer_load_lds16(__amdgpu_buffer_rsrc_t rs, cha
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16, voff, 0, 0, 0);
 }
 
-/* Eight elements of a row of `dim`, from element d on; 0 behind its end. */
-__device__ __forceinline__ u32x4_t load8(const uint16_t* row, int d, int dim, bool aligned)
+/* Eight elements of a row of `dim`, from element d on; 0 behind its end.  Rows of
+ * eight and more take one access, moved back to end with the row where it would pass
+ * it, and a shift. */
+__device__ __forceinline__ u32x4_t load8(const uint16_t* row, int d, int dim)
 {
-    u32x4_t v = {0, 0, 0, 0};
-    if (aligned && d + 8 <= dim)
-        return *reinterpret_cast<const u32x4_t*>(row + d);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (d + e < dim)
+    if (dim < 8) {
+        u32x4_t v = {0, 0, 0, 0};
+        for (int e = 0; e < dim - d; ++e)
             v[e >> 1] |= static_cast<uint32_t>(row[d + e]) << (16 * (e & 1));
-    return v;
+        return v;
+    }
+    const int start = d < dim - 8 ? d : dim - 8;
+    const u32x4_t x = *reinterpret_cast<const u32x4_any*>(row + start);
+    const int by = (d - start) * 16;   /* bits; 128 and more: nothing is left */
+    uint64_t lo = x[0] | (static_cast<uint64_t>(x[1]) << 32), hi = x[2] | (static_cast<uint64_t>(x[3]) << 32);
+    if (by >= 64) {
+        lo = by < 128 ? hi >> (by - 64) : 0;
+        hi = 0;
+    } else if (by > 0) {
+        lo = (lo >> by) | (hi << (64 - by));
+        hi >>= by;
+    }
+    return u32x4_t{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+                   static_cast<uint32_t>(hi >> 32)};
 }
 
 __device__ __forceinline__ float maximum(float a, float b) { return __builtin_elementwise_maximum(a, b); }
@@ -116,7 +131,7 @@ __device__ __forceinline__ void extent(const int32_t* cu, const int32_t* len, in
 /* DIRECT: dim == DP and every row 16-byte aligned, key tiles go straight from
  * global memory into LDS; else they pass through registers, zero-filled to DP. */
 template <bool FP16, int DP, bool DIRECT>
-__global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a, int aligned)
+__global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a)
 {
     constexpr int kSlices = DP / 16;
     constexpr int kPieces = DP / 8;
@@ -178,8 +193,12 @@ __global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a, int aligned)
             for (int s = 0; s < kSlices; ++s) {
                 if constexpr (DIRECT)
                     fq[j][s] = *reinterpret_cast<const u32x4_t*>(row + 16 * s + 8 * fhalf);
+                else if (16 * s + 16 <= a.dim)
+                    fq[j][s] = *reinterpret_cast<const u32x4_any*>(row + 16 * s + 8 * fhalf);
+                else if (s < nks)
+                    fq[j][s] = load8(row, 16 * s + 8 * fhalf, a.dim);
                 else
-                    fq[j][s] = load8(row, 16 * s + 8 * fhalf, a.dim, aligned);
+                    fq[j][s] = u32x4_t{0, 0, 0, 0};
             }
             khi[j] = len_k - 1;
             klo[j] = 0;
@@ -227,7 +246,7 @@ __global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a, int aligned)
                     const int at = c * kQkThreads + tid;
                     const int r = at / kPieces, p = at % kPieces;
                     const int rr = r < left ? r : left - 1;
-                    const u32x4_t v = load8(base + static_cast<int64_t>(rr) * a.kst, p * 8, a.dim, aligned);
+                    const u32x4_t v = load8(base + static_cast<int64_t>(rr) * a.kst, p * 8, a.dim);
                     *reinterpret_cast<u32x4_t*>(dst + piece_at<DP>(r, p)) = v;
                 }
             }
@@ -334,8 +353,8 @@ template <bool FP16, int DP>
 hipError_t launch_dim(const QkArgs& a, bool aligned, uint32_t grid, hipStream_t stream)
 {
     if (aligned && a.dim == DP)
-        return launch(k_qk_max<FP16, DP, true>, dim3(grid), kQkThreads, stream, a, 1);
-    return launch(k_qk_max<FP16, DP, false>, dim3(grid), kQkThreads, stream, a, aligned ? 1 : 0);
+        return launch(k_qk_max<FP16, DP, true>, dim3(grid), kQkThreads, stream, a);
+    return launch(k_qk_max<FP16, DP, false>, dim3(grid), kQkThreads, stream, a);
 }
 
 template <bool FP16>

@@ -22,6 +22,11 @@ namespace {
 
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+/* Four elements at any element's address: global memory takes such an access in one
+ * instruction, a line more where it straddles one. */
+typedef f32x4_t f32x4_any __attribute__((aligned(4)));
+typedef u32x2_t u32x2_any __attribute__((aligned(2)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
 
 constexpr int kRowThreads = 256;
 constexpr int kRowWaves = kRowThreads / 64;
@@ -33,11 +38,11 @@ constexpr int kMxBlock = 32;
 /* four consecutive elements of a row                                      */
 /* ---------------------------------------------------------------------- */
 /* n of them are in the row (n <= 0: none); the others read as 0 and are not written. */
-__device__ __forceinline__ f32x4_t load4(const float* p, int n, bool vec)
+__device__ __forceinline__ f32x4_t load4(const float* p, int n)
 {
     f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (vec && n >= 4)
-        return *reinterpret_cast<const f32x4_t*>(p);
+    if (n >= 4)
+        return *reinterpret_cast<const f32x4_any*>(p);
 #pragma unroll
     for (int e = 0; e < 4; ++e)
         if (e < n)
@@ -45,11 +50,11 @@ __device__ __forceinline__ f32x4_t load4(const float* p, int n, bool vec)
     return x;
 }
 
-__device__ __forceinline__ f32x4_t load4(const uint16_t* p, int n, bool vec)
+__device__ __forceinline__ f32x4_t load4(const uint16_t* p, int n)
 {
     f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (vec && n >= 4) {
-        const u32x2_t t = *reinterpret_cast<const u32x2_t*>(p);
+    if (n >= 4) {
+        const u32x2_t t = *reinterpret_cast<const u32x2_any*>(p);
         x[0] = bf16_to_f32(t.x & 0xffffu);
         x[1] = bf16_to_f32(t.x >> 16);
         x[2] = bf16_to_f32(t.y & 0xffffu);
@@ -63,10 +68,10 @@ __device__ __forceinline__ f32x4_t load4(const uint16_t* p, int n, bool vec)
     return x;
 }
 
-__device__ __forceinline__ void store4(float* p, f32x4_t x, int n, bool vec)
+__device__ __forceinline__ void store4(float* p, f32x4_t x, int n)
 {
-    if (vec && n >= 4) {
-        *reinterpret_cast<f32x4_t*>(p) = x;
+    if (n >= 4) {
+        *reinterpret_cast<f32x4_any*>(p) = x;
         return;
     }
 #pragma unroll
@@ -75,17 +80,17 @@ __device__ __forceinline__ void store4(float* p, f32x4_t x, int n, bool vec)
             p[e] = x[e];
 }
 
-__device__ __forceinline__ void store_bf16(uint16_t* p, f32x4_t x, int n, bool vec)
+__device__ __forceinline__ void store_bf16(uint16_t* p, f32x4_t x, int n)
 {
     uint32_t b[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e)
         b[e] = bf16_rne_bits(x[e]);
-    if (vec && n >= 4) {
+    if (n >= 4) {
         u32x2_t t;
         t.x = b[0] | (b[1] << 16);
         t.y = b[2] | (b[3] << 16);
-        *reinterpret_cast<u32x2_t*>(p) = t;
+        *reinterpret_cast<u32x2_any*>(p) = t;
         return;
     }
 #pragma unroll
@@ -101,7 +106,7 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, f32x4_t x, int n, bool v
  * the scale byte is that field - 8, and 0 from 2^-118 down.  Multiplying by
  * 2^-e is exact or below e4m3's smallest half step; the conversion rounds to
  * nearest even. */
-__device__ __forceinline__ void store_mx8(uint8_t* p, uint8_t* scale, f32x4_t x, int n, bool vec)
+__device__ __forceinline__ void store_mx8(uint8_t* p, uint8_t* scale, f32x4_t x, int n)
 {
     uint32_t m = 0;
 #pragma unroll
@@ -130,8 +135,8 @@ __device__ __forceinline__ void store_mx8(uint8_t* p, uint8_t* scale, f32x4_t x,
     }
     if (n > 0 && (threadIdx.x & 7) == 0)
         *scale = static_cast<uint8_t>(byte);
-    if (vec && n >= 4) {
-        *reinterpret_cast<uint32_t*>(p) = v;
+    if (n >= 4) {
+        *reinterpret_cast<u32_any*>(p) = v;
         return;
     }
 #pragma unroll
@@ -161,11 +166,11 @@ template <int PT>
 __device__ __forceinline__ void store_weight(const WeightView& w, int64_t z, const Spot& s, f32x4_t x)
 {
     if constexpr (PT == HPO_PARAM_BF16) {
-        store_bf16(static_cast<uint16_t*>(w.param.data) + z * w.param.bs + s.row * w.param.rs + s.col, x, s.n, w.vec);
+        store_bf16(static_cast<uint16_t*>(w.param.data) + z * w.param.bs + s.row * w.param.rs + s.col, x, s.n);
     } else if constexpr (PT == HPO_WEIGHT_MX8) {
         const int64_t nb = (w.cols + kMxBlock - 1) / kMxBlock;
         store_mx8(static_cast<uint8_t*>(w.param.data) + z * w.param.bs + s.row * w.param.rs + s.col,
-                  w.scales + (z * w.rows + s.row) * nb + s.col / kMxBlock, x, s.n, w.vec);
+                  w.scales + (z * w.rows + s.row) * nb + s.col / kMxBlock, x, s.n);
     }
 }
 
@@ -193,7 +198,7 @@ __global__ __launch_bounds__(kRowThreads) void k_row_stats(RmsArgs a)
 #pragma unroll 4
     for (int64_t c = 4 * (WG ? static_cast<int>(threadIdx.x) : lane); c < cols; c += step) {
         const int64_t left = cols - c;
-        const f32x4_t x = load4(o + c, left > 4 ? 4 : static_cast<int>(left), a.o_vec);
+        const f32x4_t x = load4(o + c, left > 4 ? 4 : static_cast<int>(left));
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             acc += x[e] * x[e];
@@ -265,16 +270,16 @@ __global__ __launch_bounds__(kRowThreads) void k_rms_apply(RmsArgs a)
     for (int k = 0; k < kPiecesPerWave && row < rows; ++k) {
         const Spot p = spot_of(row, piece, cols);
         const float c = static_cast<float>(s * static_cast<double>(a.r[z * rows + row]));
-        const f32x4_t o = load4(static_cast<const OT*>(a.O.data) + z * a.O.bs + row * a.O.rs + p.col, p.n, a.o_vec);
+        const f32x4_t o = load4(static_cast<const OT*>(a.O.data) + z * a.O.bs + row * a.O.rs + p.col, p.n);
         float* w = static_cast<float*>(a.w.master.data) + z * a.w.master.bs + row * a.w.master.rs + p.col;
-        f32x4_t x = load4(w, p.n, a.w.vec);
+        f32x4_t x = load4(w, p.n);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const float kept = x[e] * a.keep;
             const float u = c * o[e];
             x[e] = kept - u;
         }
-        store4(w, x, p.n, a.w.vec);
+        store4(w, x, p.n);
         store_weight<PT>(a.w, z, p, x);
         if (++piece == pieces) {
             piece = 0;
@@ -323,11 +328,11 @@ __global__ __launch_bounds__(kRowThreads) void k_qk_clip(ClipArgs a)
     for (int q = 0; q < kPiecesPerWave && row < rows; ++q) {
         const Spot p = spot_of(row, piece, cols);
         float* w = static_cast<float*>(wv.master.data) + z * wv.master.bs + row * wv.master.rs + p.col;
-        f32x4_t x = load4(w, p.n, wv.vec);
+        f32x4_t x = load4(w, p.n);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             x[e] = x[e] * f;
-        store4(w, x, p.n, wv.vec);
+        store4(w, x, p.n);
         if (wv.param_dtype == HPO_PARAM_BF16)
             store_weight<HPO_PARAM_BF16>(wv, z, p, x);
         else if (wv.param_dtype == HPO_WEIGHT_MX8)

@@ -79,14 +79,6 @@ hpo::StackView view(const hpo_stack* s)
     return v;
 }
 
-/* Every row of the stack starts on a boundary of four elements. */
-bool rows_vec4(const hpo_stack* s)
-{
-    const int64_t b = 4 * elem_size(s->dtype);
-    return aligned(s->data, static_cast<uintptr_t>(b)) && (s->batch <= 1 || s->batch_stride % 4 == 0) &&
-           (s->rows <= 1 || s->row_stride % 4 == 0);
-}
-
 /* Master and model weight of a row-wise update. */
 hpo_status weight_view(const hpo_stack* master, const hpo_stack* param, uint8_t* scales, hpo::WeightView& w)
 {
@@ -95,7 +87,6 @@ hpo_status weight_view(const hpo_stack* master, const hpo_stack* param, uint8_t*
     w.rows = master->rows;
     w.cols = master->cols;
     w.param_dtype = HPO_PARAM_FP32;
-    w.vec = rows_vec4(master) ? 1 : 0;
     if (!param) {
         if (scales)
             return fail(HPO_EINVAL, "d_scales without a param");
@@ -104,8 +95,6 @@ hpo_status weight_view(const hpo_stack* master, const hpo_stack* param, uint8_t*
     w.param_dtype = param->dtype;
     w.param = view(param);
     w.scales = scales;
-    if (!rows_vec4(param))
-        w.vec = 0;
     return HPO_OK;
 }
 
@@ -345,8 +334,6 @@ hpo_status hpo_orthogonalize(const hpo_stack* G, const hpo_stack* momentum, cons
     a.M = view(momentum);
     a.out = view(out);
     a.g_bf16 = G->dtype == HPO_PARAM_BF16 ? 1 : 0;
-    a.g_vec = rows_vec4(G) ? 1 : 0;
-    a.m_vec = momentum && rows_vec4(momentum) ? 1 : 0;
     a.use_gram = a.use_gram && std::min(G->rows, G->cols) <= hpo::kGramMax ? 1 : 0;
     a.batch = G->batch;
     a.rows = G->rows;
@@ -417,7 +404,6 @@ hpo_status hpo_rms_update(const hpo_stack* O, const hpo_stack* master, float* d_
         return st;
     a.O = view(O);
     a.o_fp32 = O->dtype == HPO_PARAM_FP32 ? 1 : 0;
-    a.o_vec = rows_vec4(O) ? 1 : 0;
     a.v = d_v;
     a.batch = master->batch;
     const int64_t n = master->batch * master->rows;

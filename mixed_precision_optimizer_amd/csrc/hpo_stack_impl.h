@@ -27,7 +27,7 @@ struct WeightView {
     uint8_t* scales;    /* HPO_WEIGHT_MX8 */
     int64_t rows, cols;
     int32_t param_dtype;   /* HPO_PARAM_FP32 (none), HPO_PARAM_BF16 or HPO_WEIGHT_MX8 */
-    int32_t vec;           /* master and param rows take 4-element accesses */
+    int32_t reserved;
 };
 
 struct RmsArgs {
@@ -42,7 +42,6 @@ struct RmsArgs {
     double gain;     /* lr * target_rms * sqrt(rows * cols) */
     float keep;      /* fp32(1 - lr * weight_decay) */
     int32_t o_fp32;
-    int32_t o_vec;   /* O rows take 4-element accesses */
     const int32_t* d_found;
 };
 
@@ -114,7 +113,6 @@ constexpr int64_t kGramMax = 128;
 struct OrthoArgs {
     StackView G, M, out;   /* M.data NULL: no momentum */
     int32_t g_bf16;
-    int32_t g_vec, m_vec;  /* rows take 4-element accesses */
     int32_t use_gram;      /* the short side fits and P stays in range */
     int32_t p_exp;         /* exponent of the final P */
     GramStep gram[HPO_NS_MAX_STEPS];
