@@ -15,7 +15,7 @@ from typing import NamedTuple, Optional, Sequence
 import torch
 
 from . import hpo
-from .hpo import HPO_PARAM_BF16, HPO_PARAM_FP16, HPO_PARAM_FP32, _check, _dptr, _flag_ptr, _norm_ptr, _stream
+from .hpo import HPO_OK, HPO_PARAM_BF16, HPO_PARAM_FP16, HPO_PARAM_FP32, _check
 
 HPO_WEIGHT_MX8 = 16
 HPO_QK_MAX_DIM = 256
@@ -81,27 +81,73 @@ _CODES = {torch.float32: HPO_PARAM_FP32, torch.bfloat16: HPO_PARAM_BF16, torch.f
           torch.float8_e4m3fn: HPO_WEIGHT_MX8}
 
 
-def _stack(t: torch.Tensor, what: str) -> c_stack:
-    hpo._on_current_device(t, what)
-    if t.dim() not in (2, 3):
-        raise ValueError(f"{what} must have 2 or 3 dimensions, got {t.dim()}")
-    if t.dtype not in _CODES:
+# These calls are a few microseconds of work on small weights, so what is done
+# per call here is kept short: one look at the current device, plain integers
+# for pointers and the stream.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _device() -> int:
+    """The current device, or -1 without one (every tensor is then refused)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -1
+
+
+def _stream(stream, dev: int):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return hpo._stream(stream)
+
+
+def _refuse_device(t: torch.Tensor, what: str, dev: int):
+    if t.get_device() < 0:
+        raise ValueError(f"{what} must be a device tensor")
+    raise ValueError(f"{what} is on {t.device} but the current device is cuda:{dev}")
+
+
+def _stack(t: torch.Tensor, what: str, dev: int) -> c_stack:
+    at = t.get_device()
+    if at != dev or at < 0:
+        _refuse_device(t, what, dev)
+    code = _CODES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{what}: {t.dtype} is not supported")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 3:
+        b, r, c = shape
+        bs, rs, cs = strides
+    elif len(shape) == 2:
+        b, bs = 1, 0
+        r, c = shape
+        rs, cs = strides
+    else:
+        raise ValueError(f"{what} must have 2 or 3 dimensions, got {len(shape)}")
+    if cs != 1 and c > 1:
         raise ValueError(f"{what}: the last dimension must be contiguous")
-    b, r, c = t.shape if t.dim() == 3 else (1, *t.shape)
-    bs, rs = (t.stride(0), t.stride(1)) if t.dim() == 3 else (0, t.stride(0))
-    return c_stack(t.data_ptr(), b, r, c, bs, rs, _CODES[t.dtype], 0)
+    return c_stack(t.data_ptr(), b, r, c, bs, rs, code, 0)
 
 
-def _opt(t: Optional[torch.Tensor], what: str):
-    return None if t is None else ctypes.byref(_stack(t, what))
+def _opt(t: Optional[torch.Tensor], what: str, dev: int):
+    return None if t is None else ctypes.byref(_stack(t, what, dev))
 
 
-def _workspace(t: Optional[torch.Tensor]):
-    if t is None:
-        return None, 0
-    return _dptr(t, "workspace"), t.numel() * t.element_size()
+def _buffer(t, what: str, dev: int, dtype, min_bytes: int):
+    """Address of a contiguous device buffer; None is NULL, an int a raw address."""
+    if t is None or isinstance(t, int):
+        return t
+    at = t.get_device()
+    if at != dev or at < 0:
+        _refuse_device(t, what, dev)
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if t.numel() * t.element_size() < min_bytes:
+        raise ValueError(f"{what} spans {t.numel() * t.element_size()} bytes, the call needs {min_bytes}")
+    return t.data_ptr()
+
+
+def _workspace(t: Optional[torch.Tensor], dev: int):
+    return (None, 0) if t is None else (_buffer(t, "workspace", dev, None, 0), t.numel() * t.element_size())
 
 
 def _shape3(t: torch.Tensor):
@@ -115,14 +161,17 @@ def mx_scales_shape(t: torch.Tensor):
     return s if t.dim() == 3 else s[1:]
 
 
-def _scales_ptr(scales: Optional[torch.Tensor], param: Optional[torch.Tensor], what: str):
+_SCALE_DTYPES = (torch.uint8, getattr(torch, "float8_e8m0fnu", torch.uint8))
+
+
+def _scales_ptr(scales: Optional[torch.Tensor], param: Optional[torch.Tensor], what: str, dev: int):
     if scales is None:
         return None
-    if scales.dtype not in (torch.uint8, getattr(torch, "float8_e8m0fnu", torch.uint8)):
+    if scales.dtype not in _SCALE_DTYPES:
         raise TypeError(f"{what} must be uint8 or float8_e8m0fnu, got {scales.dtype}")
     if param is None:
         raise ValueError(f"{what} without a param")
-    return _dptr(scales, what, None, math.prod(mx_scales_shape(param)))
+    return _buffer(scales, what, dev, None, math.prod(mx_scales_shape(param)))
 
 
 # --------------------------------------------------------------------------
@@ -141,11 +190,15 @@ def hpo_orthogonalize(G: torch.Tensor, out: torch.Tensor, cfg: hpo.hpo_muon_cfg,
     """out (bf16) = the orthogonalised Nesterov gradient of every matrix of G
     (fp32 or bf16); momentum (fp32, in place) may be left out.  The workspace is a
     uint8 device tensor of hpo_orthogonalize_workspace bytes."""
-    ws, nbytes = _workspace(workspace)
-    _check(load().hpo_orthogonalize(ctypes.byref(_stack(G, "G")), _opt(momentum, "momentum"),
-                                    ctypes.byref(_stack(out, "out")), ctypes.byref(cfg), inv_scale, max_norm,
-                                    _norm_ptr(d_norm), _flag_ptr(d_found_inf), ws, nbytes, _stream(stream)),
-           "hpo_orthogonalize")
+    dev = _device()
+    ws, nbytes = _workspace(workspace, dev)
+    st = load().hpo_orthogonalize(ctypes.byref(_stack(G, "G", dev)), _opt(momentum, "momentum", dev),
+                                  ctypes.byref(_stack(out, "out", dev)), ctypes.byref(cfg), inv_scale, max_norm,
+                                  _buffer(d_norm, "d_norm", dev, torch.float32, 4),
+                                  _buffer(d_found_inf, "d_found_inf", dev, torch.int32, 4), ws, nbytes,
+                                  _stream(stream, dev))
+    if st != HPO_OK:
+        _check(st, "hpo_orthogonalize")
 
 
 def make_rms_cfg(lr: float, weight_decay: float = 0.0, beta2: float = 0.95, eps: float = 1e-8,
@@ -167,16 +220,16 @@ def hpo_rms_update(O: torch.Tensor, master: torch.Tensor, v: Optional[torch.Tens
     """Row-normalised update of master (fp32, in place) by O (bf16 or fp32), with v
     (fp32 [batch, rows]) its running row mean squares, and the model weight:
     bf16, or float8_e4m3fn with scales (uint8 / float8_e8m0fnu, mx_scales_shape)."""
-    b, r, _ = _shape3(master)
-    ws, nbytes = _workspace(workspace)
-    _check(load().hpo_rms_update(ctypes.byref(_stack(O, "O")), ctypes.byref(_stack(master, "master")),
-                                 _dptr(v, "v", torch.float32, 4 * b * r), _opt(param, "param"),
-                                 _scales_ptr(scales, param, "scales"), ctypes.byref(cfg), _flag_ptr(d_found_inf), ws,
-                                 nbytes, _stream(stream)), "hpo_rms_update")
-
-
-def _lengths(t: Optional[torch.Tensor], what: str, n: int):
-    return _dptr(t, what, torch.int32, 4 * n)
+    dev = _device()
+    ws, nbytes = _workspace(workspace, dev)
+    w = _stack(master, "master", dev)
+    st = load().hpo_rms_update(ctypes.byref(_stack(O, "O", dev)), ctypes.byref(w),
+                               _buffer(v, "v", dev, torch.float32, 4 * w.batch * w.rows), _opt(param, "param", dev),
+                               _scales_ptr(scales, param, "scales", dev), ctypes.byref(cfg),
+                               _buffer(d_found_inf, "d_found_inf", dev, torch.int32, 4), ws, nbytes,
+                               _stream(stream, dev))
+    if st != HPO_OK:
+        _check(st, "hpo_rms_update")
 
 
 def hpo_qk_max_logits(q: torch.Tensor, k: torch.Tensor, d_max: torch.Tensor, scale: float, causal: bool = True,
@@ -186,33 +239,41 @@ def hpo_qk_max_logits(q: torch.Tensor, k: torch.Tensor, d_max: torch.Tensor, sca
     """d_max[h] (fp32) = the largest scale * (q . k) that head h sees.  q, k: bf16 or
     fp16, [batch, tokens, heads, dim] (seqlens_* int32 [batch] cut the batch rows), or
     packed [tokens, heads, dim] with cu_seqlens_* int32 [batch + 1]."""
+    dev = _device()
     packed = cu_seqlens_q is not None or cu_seqlens_k is not None
+    dims = 3 if packed else 4
+    code = _CODES.get(q.dtype)
     for what, t in (("q", q), ("k", k)):
-        hpo._on_current_device(t, what)
-        if t.dim() != (3 if packed else 4):
-            raise ValueError(f"{what} must have {3 if packed else 4} dimensions, got {t.dim()}")
-        if t.dtype not in _CODES:
-            raise TypeError(f"{what}: {t.dtype} is not supported")
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
+        if t.get_device() != dev or dev < 0:
+            _refuse_device(t, what, dev)
+        if t.dim() != dims:
+            raise ValueError(f"{what} must have {dims} dimensions, got {t.dim()}")
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError(f"{what}: the last dimension must be contiguous")
-    if q.dtype != k.dtype or q.shape[-1] != k.shape[-1] or (not packed and q.shape[0] != k.shape[0]):
-        raise ValueError(f"q {tuple(q.shape)} {q.dtype} and k {tuple(k.shape)} {k.dtype} do not go together")
+    if code is None:
+        raise TypeError(f"q: {q.dtype} is not supported")
+    qs, ks = q.shape, k.shape
+    if q.dtype != k.dtype or qs[-1] != ks[-1] or (not packed and qs[0] != ks[0]):
+        raise ValueError(f"q {tuple(qs)} {q.dtype} and k {tuple(ks)} {k.dtype} do not go together")
     if packed:
         if cu_seqlens_q is None or cu_seqlens_k is None or max_seqlen_q is None or max_seqlen_k is None:
             raise ValueError("packed sequences need cu_seqlens_q, cu_seqlens_k, max_seqlen_q and max_seqlen_k")
         batch = cu_seqlens_q.numel() - 1
         if batch < 0 or cu_seqlens_k.numel() != batch + 1:
             raise ValueError("cu_seqlens_q and cu_seqlens_k must hold batch + 1 offsets each")
+        qst, kst = (0, *q.stride()), (0, *k.stride())
     else:
-        batch = q.shape[0]
-    st = lambda t: (0, t.stride(0), t.stride(1)) if packed else (t.stride(0), t.stride(1), t.stride(2))
-    a = c_qk(q.data_ptr(), k.data_ptr(), _CODES[q.dtype], batch, q.shape[-2], k.shape[-2], q.shape[-1],
-             int(bool(causal)), window, q.shape[-3], k.shape[-3], max_seqlen_q or 0, max_seqlen_k or 0, *st(q), *st(k),
-             _lengths(cu_seqlens_q, "cu_seqlens_q", batch + 1), _lengths(cu_seqlens_k, "cu_seqlens_k", batch + 1),
-             _lengths(seqlens_q, "seqlens_q", batch), _lengths(seqlens_k, "seqlens_k", batch), scale, 0)
-    _check(load().hpo_qk_max_logits(ctypes.byref(a), int(bool(accumulate)),
-                                    _dptr(d_max, "d_max", torch.float32, 4 * q.shape[-2]), _stream(stream)),
-           "hpo_qk_max_logits")
+        batch, qst, kst = qs[0], q.stride(), k.stride()
+    lens = [None if t is None else _buffer(t, what, dev, torch.int32, n)
+            for t, what, n in ((cu_seqlens_q, "cu_seqlens_q", 4 * batch + 4), (cu_seqlens_k, "cu_seqlens_k", 4 * batch + 4),
+                               (seqlens_q, "seqlens_q", 4 * batch), (seqlens_k, "seqlens_k", 4 * batch))]
+    a = c_qk(q.data_ptr(), k.data_ptr(), code, batch, qs[-2], ks[-2], qs[-1], 1 if causal else 0, window, qs[-3],
+             ks[-3], max_seqlen_q or 0, max_seqlen_k or 0, qst[0], qst[1], qst[2], kst[0], kst[1], kst[2], *lens,
+             scale, 0)
+    st = load().hpo_qk_max_logits(ctypes.byref(a), 1 if accumulate else 0,
+                                  _buffer(d_max, "d_max", dev, torch.float32, 4 * qs[-2]), _stream(stream, dev))
+    if st != HPO_OK:
+        _check(st, "hpo_qk_max_logits")
 
 
 class ClipWeight(NamedTuple):
@@ -240,24 +301,27 @@ def _by_head(t: torch.Tensor, heads: int, what: str) -> torch.Tensor:
 def hpo_qk_clip(d_max: torch.Tensor, kv_heads: int, tau: float, weights: Sequence[ClipWeight], d_found_inf=None,
                 stream=None) -> None:
     """Rescales the rows of the heads whose d_max is over tau (in place)."""
+    dev = _device()
     n = len(weights)
     arr = (c_clip_weight * max(n, 1))()
     keep = []
     for k, w in enumerate(weights):
-        m = _by_head(w.master, w.heads, f"weights[{k}].master")
-        ms = _stack(m, f"weights[{k}].master")
+        ms = _stack(_by_head(w.master, w.heads, f"weights[{k}].master"), f"weights[{k}].master", dev)
         keep.append(ms)
-        arr[k].master = ctypes.pointer(ms)
+        c = arr[k]
+        c.master = ctypes.pointer(ms)
         if w.param is not None:
             p = _by_head(w.param, w.heads, f"weights[{k}].param")
-            ps = _stack(p, f"weights[{k}].param")
+            ps = _stack(p, f"weights[{k}].param", dev)
             keep.append(ps)
-            arr[k].param = ctypes.pointer(ps)
-            arr[k].d_scales = _scales_ptr(w.scales, p, f"weights[{k}].scales")
+            c.param = ctypes.pointer(ps)
+            c.d_scales = _scales_ptr(w.scales, p, f"weights[{k}].scales", dev)
         elif w.scales is not None:
             raise ValueError(f"weights[{k}].scales without a param")
-        arr[k].power = w.power
-        arr[k].per_group = int(bool(w.per_group))
+        c.power = w.power
+        c.per_group = 1 if w.per_group else 0
     heads = d_max.numel()
-    _check(load().hpo_qk_clip(_dptr(d_max, "d_max", torch.float32, 4 * heads), heads, kv_heads, tau, arr, n,
-                              _flag_ptr(d_found_inf), _stream(stream)), "hpo_qk_clip")
+    st = load().hpo_qk_clip(_buffer(d_max, "d_max", dev, torch.float32, 4 * heads), heads, kv_heads, tau, arr, n,
+                            _buffer(d_found_inf, "d_found_inf", dev, torch.int32, 4), _stream(stream, dev))
+    if st != HPO_OK:
+        _check(st, "hpo_qk_clip")
