@@ -34,10 +34,12 @@ struct RmsArgs {
     StackView O;
     WeightView w;
     float* v;        /* [batch][rows], nullable */
-    double* q;       /* [batch][rows] cols * ms * r^2 */
+    double* q;       /* [batch][parts] sums of cols * ms * r^2 over a part's rows */
     float* r;        /* [batch][rows] 1 / (sqrt(v) + eps) */
     double* norm2;   /* [batch], written by the fold (large stacks only) */
     int64_t batch;
+    int64_t parts;
+    int32_t rounds;  /* groups of pieces per wavefront of the update */
     double beta2, eps;
     double gain;     /* lr * target_rms * sqrt(rows * cols) */
     float keep;      /* fp32(1 - lr * weight_decay) */
@@ -51,7 +53,7 @@ struct ClipItem {
     int32_t heads;         /* matrices of the stack */
     int32_t blocks;        /* workgroups of one head */
     int32_t per_group;
-    int32_t reserved;
+    int32_t rounds;        /* groups of pieces per wavefront */
     double power;
 };
 
