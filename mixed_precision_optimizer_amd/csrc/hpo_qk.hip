@@ -128,12 +128,18 @@ __device__ __forceinline__ void extent(const int32_t* cu, const int32_t* len, in
     }
 }
 
-/* DIRECT: dim == DP and every row 16-byte aligned, key tiles go straight from
- * global memory into LDS; else they pass through registers, zero-filled to DP. */
-template <bool FP16, int DP, bool DIRECT>
+/* How key tiles come into LDS (rows of DP elements there):
+ *   kWhole    dim == DP, every row 16-byte aligned: straight from global memory;
+ *   kSlices16 dim a multiple of 16, aligned: the same, the slices behind dim hold copies of its
+ *             last piece and are not multiplied;
+ *   kAny      through registers, zero-filled to whole slices. */
+enum Mode : int { kWhole = 0, kSlices16 = 1, kAny = 2 };
+
+template <bool FP16, int DP, int MODE>
 __global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a)
 {
     constexpr int kSlices = DP / 16;
+    constexpr bool DIRECT = MODE != kAny;
     constexpr int kPieces = DP / 8;
     constexpr int kStageBytes = kTileK * DP * 2;
     constexpr int kChunks = kStageBytes / 1024 / kQkWaves;   /* 1 KB loads of a wavefront per stage */
@@ -159,7 +165,8 @@ __global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a)
     const int off = len_k - len_q;
     const uint16_t* __restrict__ Q = a.q + (a.cu_q ? 0 : b * a.qsb) + q_start * a.qst + h * a.qsh;
     const uint16_t* __restrict__ K = a.k + (a.cu_k ? 0 : b * a.ksb) + k_start * a.kst + hk * a.ksh;
-    const int nks = DIRECT ? kSlices : (a.dim + 15) / 16;   /* slices that are not all padding */
+    const int nks = MODE == kWhole ? kSlices : (a.dim + 15) / 16;   /* slices that are not all padding */
+    const int last_piece = a.dim / 8 - 1;
     const int frow = lane & 31, fhalf = lane >> 5;
     float best = -INFINITY;
 
@@ -191,8 +198,10 @@ __global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a)
             const uint16_t* row = Q + static_cast<int64_t>(i < len_q ? i : len_q - 1) * a.qst;
 #pragma unroll
             for (int s = 0; s < kSlices; ++s) {
-                if constexpr (DIRECT)
+                if constexpr (MODE == kWhole)
                     fq[j][s] = *reinterpret_cast<const u32x4_t*>(row + 16 * s + 8 * fhalf);
+                else if constexpr (MODE == kSlices16)
+                    fq[j][s] = s < nks ? *reinterpret_cast<const u32x4_t*>(row + 16 * s + 8 * fhalf) : u32x4_t{0, 0, 0, 0};
                 else if (16 * s + 16 <= a.dim)
                     fq[j][s] = *reinterpret_cast<const u32x4_any*>(row + 16 * s + 8 * fhalf);
                 else if (s < nks)
@@ -235,13 +244,17 @@ __global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a)
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) {
                     const int at = (wave * kChunks + c) * 64 + lane;
-                    const int r = at / kPieces, p = (at % kPieces) ^ swizzle<DP>(r);
+                    const int r = at / kPieces;
+                    int p = (at % kPieces) ^ swizzle<DP>(r);
+                    if constexpr (MODE == kSlices16)
+                        p = p < last_piece ? p : last_piece;
                     const int rr = r < left ? r : left - 1;
                     buffer_load_lds16(rs, dst + (wave * kChunks + c) * 1024,
                                       (rr * static_cast<int>(a.kst) + p * 8) * 2);
                 }
             } else {
-#pragma unroll
+                /* two pieces at a time: all of them in flight spill beside the queries' registers */
+#pragma unroll 2
                 for (int c = 0; c < kChunks; ++c) {
                     const int at = c * kQkThreads + tid;
                     const int r = at / kPieces, p = at % kPieces;
@@ -265,7 +278,7 @@ __global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a)
                     acc[i][j] = f32x16_t{};
 #pragma unroll
             for (int s = 0; s < kSlices; ++s) {
-                if (DIRECT || s < nks) {
+                if (MODE == kWhole || s < nks) {
                     u32x4_t fk[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
@@ -353,8 +366,10 @@ template <bool FP16, int DP>
 hipError_t launch_dim(const QkArgs& a, bool aligned, uint32_t grid, hipStream_t stream)
 {
     if (aligned && a.dim == DP)
-        return launch(k_qk_max<FP16, DP, true>, dim3(grid), kQkThreads, stream, a);
-    return launch(k_qk_max<FP16, DP, false>, dim3(grid), kQkThreads, stream, a);
+        return launch(k_qk_max<FP16, DP, kWhole>, dim3(grid), kQkThreads, stream, a);
+    if (aligned && a.dim % 16 == 0)
+        return launch(k_qk_max<FP16, DP, kSlices16>, dim3(grid), kQkThreads, stream, a);
+    return launch(k_qk_max<FP16, DP, kAny>, dim3(grid), kQkThreads, stream, a);
 }
 
 template <bool FP16>
