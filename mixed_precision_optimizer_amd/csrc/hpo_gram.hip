@@ -39,12 +39,7 @@ typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-/* four elements at any element's address (one instruction in global memory) */
-typedef f32x4_t f32x4_any __attribute__((aligned(4)));
-typedef u32x2_t u32x2_any __attribute__((aligned(2)));
 
 constexpr int kThreads = 256;
 constexpr int kTileElems = 8192;   /* elements of a column tile: 32 per thread */
@@ -93,42 +88,6 @@ __device__ __forceinline__ u32x4_t fragment(const char* base, int row0, int slic
 {
     const int lane = threadIdx.x & 63;
     return *reinterpret_cast<const u32x4_t*>(base + piece_at<ROW>(row0 + (lane & 31), 2 * slice + (lane >> 5)));
-}
-
-/* Four consecutive stored elements: n of them are there (the others read as 0). */
-template <bool BF16>
-__device__ __forceinline__ f32x4_t grad4(const OrthoSrc& s, int64_t at, int n)
-{
-    f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (n >= 4) {
-        if constexpr (BF16) {
-            const u32x2_t t = *reinterpret_cast<const u32x2_any*>(static_cast<const uint16_t*>(s.G) + at);
-            x[0] = bf16_to_f32(t.x & 0xffffu);
-            x[1] = bf16_to_f32(t.x >> 16);
-            x[2] = bf16_to_f32(t.y & 0xffffu);
-            x[3] = bf16_to_f32(t.y >> 16);
-        } else {
-            x = *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(s.G) + at);
-        }
-        return x;
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (e < n)
-            x[e] = src_at<BF16>(s, at + e);
-    return x;
-}
-
-__device__ __forceinline__ f32x4_t momentum4(const OrthoSrc& s, int64_t at, int n)
-{
-    f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (n >= 4)
-        return *reinterpret_cast<const f32x4_any*>(s.M + at);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (e < n)
-            x[e] = s.M[at + e];
-    return x;
 }
 
 /* A thread's share of one column tile, as eight runs of four elements that lie
@@ -227,15 +186,7 @@ __device__ __forceinline__ void finish(const GramArgs& a, const GradVals& k, int
                 for (int e = 0; e < 4; ++e)
                     x.m[j][e] = s.sc.form == HPO_MUON_MOMENTUM_SUM ? s.sc.mu * x.m[j][e] + x.g[j][e]
                                                                     : s.sc.mu * x.m[j][e] + s.sc.omu * x.g[j][e];
-                float* M = s.M + z * s.mbs + row * s.mrs + col;
-                if (cnt >= 4) {
-                    *reinterpret_cast<f32x4_any*>(M) = x.m[j];
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (e < cnt)
-                            M[e] = x.m[j][e];
-                }
+                put_momentum4(s, z * s.mbs + row * s.mrs + col, cnt, x.m[j]);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e)

@@ -68,8 +68,6 @@ typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
-typedef float f32x4_t __attribute__((ext_vector_type(4)));
 
 /* Pin the interleave of fragment reads and MFMAs with scheduling barriers. */
 #ifndef HPO_NS_SCHED
@@ -602,6 +600,29 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
 #endif
     };
     const int nk = g.K / kBK;
+    /* On small grids a launch is a chain of latencies: the epilogue's input tile (and, for the step,
+     * what the rounding lost) is asked for before the k-loop and waits in registers. */
+    constexpr bool kEarly = kBM == 64 && EPI != kEpiF16Gram;
+    constexpr int kEarlyPieces = kBN * kBM / 8 / kNsThreads;
+    u32x4_t early[kEarly ? kEarlyPieces : 1];
+    u32x2_t early_lo[kEarly && EPI == kEpiF16Step ? 4 : 1];
+    if constexpr (kEarly) {
+        const uint16_t* src = EPI == kEpiF16Poly ? g.P + z * g.sp + col0 * g.ldp + row0
+                                                 : g.XS + z * g.sxs + col0 * g.ldxs + row0;
+        const int64_t ld = EPI == kEpiF16Poly ? g.ldp : g.ldxs;
+#pragma unroll
+        for (int k = 0; k < kEarlyPieces; ++k) {
+            const int idx = tid + k * kNsThreads, j = idx / (kBM / 8), i = (idx % (kBM / 8)) * 8;
+            early[k] = *reinterpret_cast<const u32x4_t*>(src + j * ld + i);
+        }
+        if constexpr (EPI == kEpiF16Step) {
+            const u32x2_t* lo = reinterpret_cast<const u32x2_t*>(g.XL + z * g.sxl) +
+                                ((ty * g.nx + tx) * T::kWaves + wave) * (kTM * kTN * 4 * 64) + lane;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                early_lo[q] = lo[q * 64];
+        }
+    }
     /* the cross-barrier pipeline needs two stages of four k-slices */
     constexpr bool kXbar = HPO_NS_XBAR && kBK == 64 && kStages == 2;
     if constexpr (kXbar) {
@@ -802,7 +823,10 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
 #pragma clang loop unroll(full)
             for (int k = 0; k < kEpiPieces; ++k) {
                 const int idx = tid + k * kNsThreads, j = idx / kCPR, i = (idx % kCPR) * 8;
-                v[k] = *reinterpret_cast<const u32x4_t*>(src + j * ld + i);
+                if constexpr (kEarly)
+                    v[k] = early[k];
+                else
+                    v[k] = *reinterpret_cast<const u32x4_t*>(src + j * ld + i);
             }
 #pragma clang loop unroll(full)
             for (int k = 0; k < kEpiPieces; ++k) {
@@ -954,7 +978,7 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
                     u32x2_t lv[4];
 #pragma clang loop unroll(full)
                     for (int q = 0; q < 4; ++q)
-                        lv[q] = lo[((ti * kTN + tj) * 4 + q) * 64];
+                        lv[q] = kEarly ? early_lo[kEarly ? q : 0] : lo[((ti * kTN + tj) * 4 + q) * 64];
 #pragma clang loop unroll(full)
                     for (int q = 0; q < 4; ++q) {
                         const int i = wm + 32 * ti + 8 * q + lrow4, j = wn + 32 * tj + lcol;
@@ -1278,33 +1302,45 @@ __global__ __launch_bounds__(kSumThreads) void k_stack_momentum(OrthoSrc s, doub
 {
     if (!gate_open(s.sc.gate))
         return;
-    const GradVals k = grad_vals(s.sc);
+    const GradVals v = grad_vals(s.sc);
     const int64_t z = blockIdx.y;
     double acc = 0.0;
-    /* rows are handed out by wavefront: one row at a time, 64 consecutive elements an access */
+    /* a wavefront takes a run of 1024 columns of one row, four elements a lane and access */
     const int64_t wave = static_cast<int64_t>(blockIdx.x) * (kSumThreads / 64) + (threadIdx.x >> 6);
     const int64_t waves = static_cast<int64_t>(gridDim.x) * (kSumThreads / 64);
     const int lane = threadIdx.x & 63;
-    /* a wavefront takes a run of 1024 columns of one row */
     constexpr int64_t kRun = 1024;
     const int64_t runs = (s.cols + kRun - 1) / kRun;
     for (int64_t t = wave; t < s.rows * runs; t += waves) {
-        const int64_t i = t / runs, c0 = (t % runs) * kRun;
-        const int64_t c1 = c0 + kRun < s.cols ? c0 + kRun : s.cols;
+        const int64_t i = t / runs, c0 = (t % runs) * kRun + 4 * lane;
         const int64_t g0 = z * s.gbs + i * s.grs, m0 = z * s.mbs + i * s.mrs;
-#pragma unroll 4
-        for (int64_t c = c0 + lane; c < c1; c += 64) {
-            float g = src_at<BF16>(s, g0 + c) * k.inv_scale;
-            if (k.clip)
-                g = g * k.C;
-            float gt = g;
-            if (s.M != nullptr) {
-                float M = s.M[m0 + c];
-                M = s.sc.form == HPO_MUON_MOMENTUM_SUM ? s.sc.mu * M + g : s.sc.mu * M + s.sc.omu * g;
-                s.M[m0 + c] = M;
-                gt = nesterov_of(g, M, s.sc);
+        f32x4_t g4[kRun / 256], m4[kRun / 256];
+#pragma unroll
+        for (int k = 0; k < kRun / 256; ++k) {
+            g4[k] = grad4<BF16>(s, g0 + c0 + 256 * k, s.cols - (c0 + 256 * k));
+            if (s.M != nullptr)
+                m4[k] = momentum4(s, m0 + c0 + 256 * k, s.cols - (c0 + 256 * k));
+        }
+#pragma unroll
+        for (int k = 0; k < kRun / 256; ++k) {
+            const int64_t left = s.cols - (c0 + 256 * k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float g = g4[k][e] * v.inv_scale;
+                if (v.clip)
+                    g = g * v.C;
+                float gt = g;
+                if (s.M != nullptr) {
+                    float M = m4[k][e];
+                    M = s.sc.form == HPO_MUON_MOMENTUM_SUM ? s.sc.mu * M + g : s.sc.mu * M + s.sc.omu * g;
+                    m4[k][e] = M;
+                    gt = nesterov_of(g, M, s.sc);
+                }
+                if (e < left)
+                    acc += static_cast<double>(gt) * static_cast<double>(gt);
             }
-            acc += static_cast<double>(gt) * static_cast<double>(gt);
+            if (s.M != nullptr)
+                put_momentum4(s, m0 + c0 + 256 * k, left, m4[k]);
         }
     }
     const double tot = block_sum<kSumThreads>(acc);
@@ -1358,28 +1394,35 @@ __global__ __launch_bounds__(kBlock) void k_stack_input(OrthoSrc s, const double
         dnorm = static_cast<float>(sqrt(tot)) + s.sc.eps;
     __syncthreads();
     const float d = dnorm;
-    constexpr int kPer = kTile * kTile / kBlock;
-    float x[kPer];
+    constexpr int kPer = kTile * kTile / 4 / kBlock;
+    f32x4_t x[kPer], mom[kPer];
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
         const int e = tid + q * kBlock;
-        const int64_t gr = r0 + e / kTile, gc = c0 + e % kTile;
-        x[q] = 0.0f;
-        if (gr < s.rows && gc < s.cols) {
-            float g = src_at<BF16>(s, z * s.gbs + gr * s.grs + gc) * k.inv_scale;
-            if (k.clip)
-                g = g * k.C;
-            x[q] = s.M != nullptr ? nesterov_of(g, s.M[z * s.mbs + gr * s.mrs + gc], s.sc) : g;
-        }
+        const int64_t gr = r0 + e / (kTile / 4), gc = c0 + e % (kTile / 4) * 4;
+        const int64_t left = gr < s.rows ? s.cols - gc : 0;
+        x[q] = grad4<BF16>(s, z * s.gbs + gr * s.grs + gc, left);
+        if (s.M != nullptr)
+            mom[q] = momentum4(s, z * s.mbs + gr * s.mrs + gc, left);
     }
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
         const int e = tid + q * kBlock;
-        /* 0 / 0 is a matrix of zeros with eps = 0: it stays 0 */
-        const float y = (x[q] == 0.0f ? 0.0f : x[q] / d) * x0_scale;
-        const uint32_t h = f16_bits(y);
-        tile[e / kTile][e % kTile] = static_cast<uint16_t>(h);
-        tlo[e / kTile][e % kTile] = static_cast<uint16_t>(f16_bits((y - f16v(static_cast<uint16_t>(h))) * kLoScale));
+        const int r = e / (kTile / 4), c = e % (kTile / 4) * 4;
+        const int64_t left = r0 + r < s.rows ? s.cols - (c0 + c) : 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            float g = x[q][t] * k.inv_scale;
+            if (k.clip)
+                g = g * k.C;
+            if (s.M != nullptr)
+                g = nesterov_of(g, mom[q][t], s.sc);
+            /* 0 / 0 is a matrix of zeros with eps = 0: it stays 0, as does what lies behind the edge */
+            const float y = g == 0.0f || t >= left ? 0.0f : g / d * x0_scale;
+            const uint32_t h = f16_bits(y);
+            tile[r][c + t] = static_cast<uint16_t>(h);
+            tlo[r][c + t] = static_cast<uint16_t>(f16_bits((y - f16v(static_cast<uint16_t>(h))) * kLoScale));
+        }
     }
     __syncthreads();
     auto row8 = [&](const uint16_t(*t)[kTile + 2], int r, int p) {

@@ -108,6 +108,60 @@ __device__ __forceinline__ float nesterov_of(float g, float M, const MuonScalars
     return sc.form == HPO_MUON_MOMENTUM_SUM ? g + sc.mu * M : sc.omu * g + sc.mu * M;
 }
 
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+/* four elements at any element's address (one instruction in global memory) */
+typedef f32x4_t f32x4_any __attribute__((aligned(4)));
+typedef u32x2_t u32x2_any __attribute__((aligned(2)));
+
+/* Four consecutive stored elements: n of them are there (the others read as 0). */
+template <bool BF16>
+__device__ __forceinline__ f32x4_t grad4(const OrthoSrc& s, int64_t at, int64_t n)
+{
+    f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n >= 4) {
+        if constexpr (BF16) {
+            const u32x2_t t = *reinterpret_cast<const u32x2_any*>(static_cast<const uint16_t*>(s.G) + at);
+            x[0] = bf16_to_f32(t.x & 0xffffu);
+            x[1] = bf16_to_f32(t.x >> 16);
+            x[2] = bf16_to_f32(t.y & 0xffffu);
+            x[3] = bf16_to_f32(t.y >> 16);
+        } else {
+            x = *reinterpret_cast<const f32x4_any*>(static_cast<const float*>(s.G) + at);
+        }
+        return x;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < n)
+            x[e] = src_at<BF16>(s, at + e);
+    return x;
+}
+
+__device__ __forceinline__ f32x4_t momentum4(const OrthoSrc& s, int64_t at, int64_t n)
+{
+    f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (n >= 4)
+        return *reinterpret_cast<const f32x4_any*>(s.M + at);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < n)
+            x[e] = s.M[at + e];
+    return x;
+}
+
+__device__ __forceinline__ void put_momentum4(const OrthoSrc& s, int64_t at, int64_t n, f32x4_t x)
+{
+    if (n >= 4) {
+        *reinterpret_cast<f32x4_any*>(s.M + at) = x;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (e < n)
+            s.M[at + e] = x[e];
+}
+
 __device__ __forceinline__ uint32_t f16_bits(float x)
 {
     return __builtin_bit_cast(uint16_t, static_cast<_Float16>(x));
