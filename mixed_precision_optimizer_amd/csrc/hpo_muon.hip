@@ -341,6 +341,8 @@ enum Epi : int {
     kEpiF16Poly = 6, /* C = f16(b * P[i][j] + c * acc) */
     kEpiF16Step = 7, /* x = a * (X + XL 2^-11) + c * acc; X = f16(x) in place, X^T, XL = f16((x - X) 2^11) */
     kEpiF16Out = 8,  /* bf16(a * X + c * acc) -> out16, natural layout */
+    kEpiF16Part = 9, /* acc over a part of k -> part, in the order of the registers */
+    kEpiF16Sum = 10, /* no product: the parts' sum as kEpiF16Gram's acc */
 };
 
 /* 2^11: fp16 keeps 11 bits, so what a rounding loses is held again at full precision. */
@@ -380,6 +382,8 @@ struct GemmArgs {
     int32_t lo_out;      /* f16 step: the next step wants it (written in place) */
     uint16_t* out16;     /* f16 out: bf16 result */
     int64_t oss, ors;    /* its matrix and row strides */
+    float* part;         /* f16 part / sum: [matrix][part of k][tile][register order] */
+    int32_t kparts;
     const TensorDesc* desc;
     const MuonInfo* info;
     MuonGate gate;
@@ -498,8 +502,16 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
     tile_of<SYM>(g, ty, tx);
     const int64_t row0 = ty * kBM;
     const int64_t col0 = tx * kBN;
-    const uint16_t* __restrict__ P = g.P + z * g.sp + row0 * g.ldp;
-    const uint16_t* __restrict__ Q = g.Q + z * g.sq + col0 * g.ldq;
+    /* a part of k: whole pairs of stages (the pipelined loop's trip) */
+    int64_t k_first = 0, k_count = g.K;
+    if constexpr (EPI == kEpiF16Part) {
+        constexpr int kUnit = kBM == 64 ? kBK : 2 * kBK;
+        const int64_t units = g.K / kUnit, s = blockIdx.y;
+        k_first = units * s / g.kparts * kUnit;
+        k_count = units * (s + 1) / g.kparts * kUnit - k_first;
+    }
+    const uint16_t* __restrict__ P = g.P + z * g.sp + row0 * g.ldp + k_first;
+    const uint16_t* __restrict__ Q = g.Q + z * g.sq + col0 * g.ldq + k_first;
     const int tid = threadIdx.x;
     /* the wavefront index is uniform: keep it scalar so chunk choices, descriptors and the LDS
      * destination of each load stay in SGPRs */
@@ -599,10 +611,10 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
         __builtin_amdgcn_s_setprio(0);
 #endif
     };
-    const int nk = g.K / kBK;
+    const int nk = static_cast<int>(k_count / kBK);
     /* On small grids a launch is a chain of latencies: the epilogue's input tile (and, for the step,
      * what the rounding lost) is asked for before the k-loop and waits in registers. */
-    constexpr bool kEarly = kBM == 64 && EPI != kEpiF16Gram;
+    constexpr bool kEarly = kBM == 64 && (EPI == kEpiF16Poly || EPI == kEpiF16Step || EPI == kEpiF16Out);
     constexpr int kEarlyPieces = kBN * kBM / 8 / kNsThreads;
     u32x4_t early[kEarly ? kEarlyPieces : 1];
     u32x2_t early_lo[kEarly && EPI == kEpiF16Step ? 4 : 1];
@@ -625,7 +637,29 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
     }
     /* the cross-barrier pipeline needs two stages of four k-slices */
     constexpr bool kXbar = HPO_NS_XBAR && kBK == 64 && kStages == 2;
-    if constexpr (kXbar) {
+    /* where the registers of this thread lie in a part, in units of four */
+    auto part_of = [&](int64_t s) {
+        const int64_t tiles = static_cast<int64_t>(g.nt) * (g.nt + 1) / 2;
+        const int64_t tile = ty * g.nt - ty * (ty - 1) / 2 + tx - ty;
+        return reinterpret_cast<f32x4_t*>(g.part) + ((z * g.kparts + s) * tiles + tile) * (kBM * kBN / 4) +
+               wave * (kTM * kTN * 4 * 64) + lane;
+    };
+    if constexpr (EPI == kEpiF16Sum) {
+        for (int s = 0; s < g.kparts; ++s) {
+            const f32x4_t* src = part_of(s);
+#pragma unroll
+            for (int i = 0; i < kTM; ++i)
+#pragma unroll
+                for (int j = 0; j < kTN; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const f32x4_t x = src[((i * kTN + j) * 4 + q) * 64];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[i][j][4 * q + e] += x[e];
+                    }
+        }
+    } else if constexpr (kXbar) {
         /* Two stages, the barrier moved inside the stream of k-slices.  The
          * fragments of slice kk + 1 are read while the MFMAs of slice kk run, across
          * stage boundaries too: before the last slice of stage kt (its fragments
@@ -781,6 +815,23 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
         }
     }
 
+    if constexpr (EPI == kEpiF16Part) {
+        f32x4_t* dst = part_of(blockIdx.y);
+#pragma unroll
+        for (int i = 0; i < kTM; ++i)
+#pragma unroll
+            for (int j = 0; j < kTN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    f32x4_t x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = acc[i][j][4 * q + e];
+                    dst[((i * kTN + j) * 4 + q) * 64] = x;
+                }
+        return;
+    }
+
     /* Staged epilogue.  acc[ti][tj][r] holds C[i][j] (tile coordinates) with
      * i = wm + 32 ti + 8 (r / 4) + 4 (lane / 32) + r % 4 and
      * j = wn + 32 tj + lane % 32: four consecutive rows of one column per
@@ -885,7 +936,8 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
         };
         __builtin_amdgcn_s_waitcnt(0);
         __syncthreads();   /* every wavefront is past its last fragment read */
-        if constexpr (EPI == kEpiGram || EPI == kEpiPoly || EPI == kEpiF16Gram || EPI == kEpiF16Poly) {
+        if constexpr (EPI == kEpiGram || EPI == kEpiPoly || EPI == kEpiF16Gram || EPI == kEpiF16Poly ||
+                      EPI == kEpiF16Sum) {
             constexpr bool kPoly = EPI == kEpiPoly || EPI == kEpiF16Poly;
             const bool diag = SYM && ty == tx;
             if constexpr (kPoly) {
@@ -905,7 +957,7 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
 #pragma clang loop unroll(full)
                         for (int e = 0; e < 4; ++e)
                             x[e] = acc[ti][tj][4 * q + e];
-                        if constexpr (EPI == kEpiF16Gram) {
+                        if constexpr (EPI == kEpiF16Gram || EPI == kEpiF16Sum) {
 #pragma clang loop unroll(full)
                             for (int e = 0; e < 4; ++e)
                                 x[e] = g.c * x[e];
@@ -1476,6 +1528,7 @@ struct OrthoPlan {
     int64_t slot;      /* bytes of one matrix */
     int64_t count;     /* matrices of a slice */
     int32_t tile;      /* GEMM tile side */
+    int32_t kparts;    /* parts that the Gram product's k is cut into */
 };
 
 int64_t pad_to(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
@@ -1485,20 +1538,42 @@ int64_t pad_to(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
  * workgroup per CU beyond.  Fitted to 19 shapes from 256 x 256 to 4096 x 4096 in stacks of
  * 1 to 64 on each tile, five steps each: 1 x 1024 x 1024 takes 461 / 283 / 164 us with
  * 256 / 128 / 64, 2 x 2048 x 2048 739 / 578 / 782, 1 x 4096 x 4096 1624 / 1856 / 2788. */
-double step_us(int64_t batch, int64_t m, int64_t n, int64_t t)
+double launch_us(int64_t t, double wgs, double depth, bool general)
 {
     constexpr double kCus = 256.0;
+    if (t == GenTile::kBM)   /* one workgroup a CU: the general product's stores are not overlapped */
+        return 12.5 + (general ? 20.0 * std::min(1.0, wgs / kCus) : 0.0) + 0.0167 * depth * std::ceil(wgs / kCus);
+    if (t == MidTile::kBM)
+        return 7.0 + depth * (wgs <= kCus ? 0.0102 : 0.0085 * std::ceil(wgs / kCus));
+    return 3.2 + depth * (wgs <= 2 * kCus ? 0.0062 : 0.0038 * std::ceil(wgs / kCus));
+}
+
+/* The Gram product (a triangle of tiles, all of n deep) leaves CUs idle on lone matrices; its k
+ * cut into parts fills them, for a second launch that sums the fp32 parts (written and read
+ * once, about 5 TB/s).  4096 x 14336: 298 us whole. */
+double gram_us(int64_t batch, int64_t m, int64_t n, int64_t t, int32_t parts)
+{
+    const double mt = static_cast<double>(pad_to(m, t) / t), np = static_cast<double>(pad_to(n, t));
+    const double tri = static_cast<double>(batch) * mt * (mt + 1.0) / 2.0, side = static_cast<double>(t);
+    const double us = launch_us(t, tri * parts, np / parts, false);
+    return parts == 1 ? us : us + 4.0 + tri * parts * side * side * 8.0 / 5e6;
+}
+
+int32_t pick_parts(int64_t batch, int64_t m, int64_t n, int64_t t)
+{
+    int32_t best = 1;
+    for (int32_t p = 2; p <= 16 && pad_to(n, t) / p >= 256; ++p)
+        if (gram_us(batch, m, n, t, p) < 0.9 * gram_us(batch, m, n, t, best))
+            best = p;
+    return best;
+}
+
+double step_us(int64_t batch, int64_t m, int64_t n, int64_t t)
+{
     const double mt = static_cast<double>(pad_to(m, t) / t), nt = static_cast<double>(pad_to(n, t) / t);
     const double b = static_cast<double>(batch), k = static_cast<double>(t);
-    auto launch_us = [&](double wgs, double depth, bool general) {
-        if (t == GenTile::kBM)   /* one workgroup a CU: the general product's stores are not overlapped */
-            return 12.5 + (general ? 20.0 * std::min(1.0, wgs / kCus) : 0.0) + 0.0167 * depth * std::ceil(wgs / kCus);
-        if (t == MidTile::kBM)
-            return 7.0 + depth * (wgs <= kCus ? 0.0102 : 0.0085 * std::ceil(wgs / kCus));
-        return 3.2 + depth * (wgs <= 2 * kCus ? 0.0062 : 0.0038 * std::ceil(wgs / kCus));
-    };
-    const double tri = b * mt * (mt + 1.0) / 2.0;
-    return launch_us(tri, k * nt, false) + launch_us(tri, k * mt, false) + launch_us(b * mt * nt, k * mt, true);
+    return gram_us(batch, m, n, t, pick_parts(batch, m, n, t)) +
+           launch_us(t, b * mt * (mt + 1.0) / 2.0, k * mt, false) + launch_us(t, b * mt * nt, k * mt, true);
 }
 
 int32_t pick_tile(int64_t batch, int64_t m, int64_t n)
@@ -1519,7 +1594,11 @@ OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols)
     p.mp = pad_to(p.m, p.tile);
     p.np = pad_to(p.n, p.tile);
     p.parts = sum_parts(rows, cols);
+    p.kparts = pick_parts(batch, p.m, p.n, p.tile);
+    const int64_t mt = p.mp / p.tile;
     p.slot = 2 * (4 * p.mp * p.np + 2 * p.mp * p.mp);
+    if (p.kparts > 1)
+        p.slot += 4 * p.kparts * (mt * (mt + 1) / 2) * p.tile * p.tile;
     /* slices of equal size under the cap (one matrix at the least) */
     constexpr int64_t kCap = int64_t{4} << 30;
     const int64_t most = kCap / p.slot > 1 ? kCap / p.slot : 1;
@@ -1550,6 +1629,7 @@ hipError_t ortho_slice(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64
     w.XL = take(xs);
     w.A = take(as);
     w.B = take(as);
+    float* part = reinterpret_cast<float*>(at);
     const OrthoSrc s = slice_of(a, z0);
     const uint32_t cnt = static_cast<uint32_t>(count);
     hipError_t e = launch3(k_stack_momentum<BF16>, dim3(static_cast<uint32_t>(p.parts), cnt), kSumThreads, stream, s,
@@ -1580,7 +1660,18 @@ hipError_t ortho_slice(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64
         g.c = f.gram;
         g.nt = static_cast<int32_t>(p.mp / T::kBM);
         const dim3 tri(static_cast<uint32_t>(g.nt * (g.nt + 1) / 2), 1, cnt);
-        e = launch3(k_ns_gemm<kEpiF16Gram, true, T>, tri, T::kThreads, stream, g, up);
+        if (p.kparts > 1) {
+            g.part = part;
+            g.kparts = p.kparts;
+            dim3 cut = tri;
+            cut.y = static_cast<uint32_t>(p.kparts);
+            e = launch3(k_ns_gemm<kEpiF16Part, true, T>, cut, T::kThreads, stream, g, up);
+            if (e != hipSuccess)
+                return e;
+            e = launch3(k_ns_gemm<kEpiF16Sum, true, T>, tri, T::kThreads, stream, g, up);
+        } else {
+            e = launch3(k_ns_gemm<kEpiF16Gram, true, T>, tri, T::kThreads, stream, g, up);
+        }
         if (e != hipSuccess)
             return e;
         g.P = w.A; g.ldp = p.mp; g.sp = as;
