@@ -288,14 +288,17 @@ class ClipWeight(NamedTuple):
     per_group: bool = True
 
 
-def _by_head(t: torch.Tensor, heads: int, what: str) -> torch.Tensor:
+def _head_stack(t: torch.Tensor, heads: int, what: str, dev: int) -> c_stack:
+    """t as a stack of one matrix per head: [heads * dim, cols] or [heads, dim, cols]."""
+    s = _stack(t, what, dev)
     if t.dim() == 2:
-        if heads < 1 or t.shape[0] % heads:
-            raise ValueError(f"{what}: {t.shape[0]} rows are not {heads} heads")
-        return t.unflatten(0, (heads, t.shape[0] // heads))
-    if t.dim() != 3 or t.shape[0] != heads:
+        if heads < 1 or s.rows % heads:
+            raise ValueError(f"{what}: {s.rows} rows are not {heads} heads")
+        s.batch, s.rows = heads, s.rows // heads
+        s.batch_stride = s.rows * s.row_stride
+    elif s.batch != heads:
         raise ValueError(f"{what} must be [{heads} * dim, cols] or [{heads}, dim, cols], got {tuple(t.shape)}")
-    return t
+    return s
 
 
 def hpo_qk_clip(d_max: torch.Tensor, kv_heads: int, tau: float, weights: Sequence[ClipWeight], d_found_inf=None,
@@ -306,18 +309,17 @@ def hpo_qk_clip(d_max: torch.Tensor, kv_heads: int, tau: float, weights: Sequenc
     arr = (c_clip_weight * max(n, 1))()
     keep = []
     for k, w in enumerate(weights):
-        ms = _stack(_by_head(w.master, w.heads, f"weights[{k}].master"), f"weights[{k}].master", dev)
+        what = f"weights[{k}]."
+        ms = _head_stack(w.master, w.heads, what + "master", dev)
         keep.append(ms)
         c = arr[k]
         c.master = ctypes.pointer(ms)
         if w.param is not None:
-            p = _by_head(w.param, w.heads, f"weights[{k}].param")
-            ps = _stack(p, f"weights[{k}].param", dev)
+            ps = _head_stack(w.param, w.heads, what + "param", dev)
             keep.append(ps)
             c.param = ctypes.pointer(ps)
-            c.d_scales = _scales_ptr(w.scales, p, f"weights[{k}].scales", dev)
-        elif w.scales is not None:
-            raise ValueError(f"weights[{k}].scales without a param")
+        if w.scales is not None:
+            c.d_scales = _scales_ptr(w.scales, w.param, what + "scales", dev)
         c.power = w.power
         c.per_group = 1 if w.per_group else 0
     heads = d_max.numel()
