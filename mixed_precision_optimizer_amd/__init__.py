@@ -5,6 +5,6 @@ libhpo.so (C ABI in include/hpo.h, HIP kernels in csrc/) does all the work;
 do.  `inputs` draws the seeded synthetic workloads.
 """
 from . import hpo, hpo_stack  # noqa: F401
-from .optimizer import DeviceAdamW, MixedPrecisionAdamW  # noqa: F401
+from .optimizer import DeviceAdamW, MixedPrecisionAdamW, StackMuon  # noqa: F401
 
-__all__ = ["hpo", "hpo_stack", "MixedPrecisionAdamW", "DeviceAdamW"]
+__all__ = ["hpo", "hpo_stack", "MixedPrecisionAdamW", "DeviceAdamW", "StackMuon"]

@@ -19,7 +19,7 @@ from typing import Optional, Sequence, Tuple
 import numpy as np
 import torch
 
-from . import hpo
+from . import hpo, hpo_stack
 
 
 class MixedPrecisionAdamW:
@@ -160,3 +160,48 @@ class DeviceAdamW:
         self.t_first = st.applied_steps + 1
         self.pending = 0
         return st
+
+
+class StackMuon:
+    """Muon for one weight that is a stack of matrices (the heads of a
+    projection, the experts of a layer): `master` is fp32 [batch, rows, cols]
+    (or one matrix [rows, cols]), `param` its model weight (bf16, or
+    float8_e4m3fn with `scales`; None: the master is the weight).  A step is the
+    momentum, Newton-Schulz of every matrix, and the update with each row
+    divided by the root of its running mean square, scaled to an update of root
+    mean square lr * target_rms.  Everything is enqueued on the current stream;
+    nothing is read back.  The momentum, the row statistics, the orthogonalised
+    update and the workspaces belong to the object: steps of one object are
+    ordered on one stream, and a captured step is replayed only while the
+    object lives.
+    """
+
+    def __init__(self, master: torch.Tensor, param: Optional[torch.Tensor] = None,
+                 scales: Optional[torch.Tensor] = None, *, lr: float, weight_decay: float = 0.0,
+                 momentum: float = 0.95, nesterov: bool = True, ns_steps: int = 5, ns_coeffs=None,
+                 beta2: float = 0.95, eps: float = 1e-8, target_rms: float = 0.2):
+        self.master, self.param, self.scales = master, param, scales
+        self.muon = hpo.make_muon_cfg(momentum=momentum, nesterov=nesterov, ns_steps=ns_steps, ns_coeffs=ns_coeffs)
+        self.rms = hpo_stack.make_rms_cfg(lr, weight_decay, beta2, eps, target_rms)
+        dev = master.device
+        self.momentum = torch.zeros(master.shape, dtype=torch.float32, device=dev)
+        self.v = torch.zeros(master.shape[:-1], dtype=torch.float32, device=dev)
+        self.update = torch.empty(master.shape, dtype=torch.bfloat16, device=dev)
+        self._ws = torch.empty(max(hpo_stack.hpo_orthogonalize_workspace(master),
+                                   hpo_stack.hpo_rms_update_workspace(master)), dtype=torch.uint8, device=dev)
+
+    def step(self, grad: torch.Tensor, *, lr: Optional[float] = None, inv_scale: float = 1.0, max_norm: float = 0.0,
+             d_norm=None, d_found_inf=None) -> None:
+        """One step from the stored grad (fp32 or bf16, master's shape).  inv_scale,
+        the clip by d_norm and the skip on d_found_inf are the chain's, as in
+        hpo_muon_step; a skipped step changes nothing."""
+        if lr is not None:
+            self.rms.lr = lr
+        hpo_stack.hpo_orthogonalize(grad, self.update, self.muon, self._ws, self.momentum, inv_scale, max_norm, d_norm,
+                                    d_found_inf)
+        hpo_stack.hpo_rms_update(self.update, self.master, self.v, self.rms, self._ws, self.param, self.scales,
+                                 d_found_inf)
+
+    def clip_weight(self, power: float = 0.5, per_group: bool = True) -> hpo_stack.ClipWeight:
+        """This weight for hpo_qk_clip, one matrix of the stack per head."""
+        return hpo_stack.ClipWeight(self.master, self.master.shape[0], power, self.param, self.scales, per_group)

@@ -667,3 +667,92 @@ def test_a_muon_clip_step(S):
     for m in base:
         for key in ("W", "p", "M", "v", "O"):
             assert torch.equal(su.bits(a[m][key]), su.bits(b[m][key])), (m, key)
+
+
+def test_stack_muon_is_its_two_calls(S):
+    """StackMuon steps, skips and clips as the calls do, bit for bit, with an 8-bit weight."""
+    from mixed_precision_optimizer_amd import StackMuon
+    b, r, c = 4, 24, 160
+    W0 = 0.02 * torch.randn(b, r, c, generator=gen(81))
+    W1, W2 = W0.to(DEV), W0.to(DEV)
+    p1, s1 = make_param("mx8", (b, r, c))
+    p2, s2 = make_param("mx8", (b, r, c))
+    opt = StackMuon(W1, p1.view, s1, lr=0.02, weight_decay=0.1)
+    cfg, rcfg = S.hpo.make_muon_cfg(), S.make_rms_cfg(0.02, 0.1)
+    M, v = torch.zeros_like(W2), torch.zeros(b, r, device=DEV)
+    flag, norm = torch.zeros(1, dtype=torch.int32, device=DEV), torch.tensor([4.0], device=DEV)
+    for k in range(3):
+        G = gradient(82 + k, b, r, c).bfloat16().to(DEV)
+        flag.fill_(k == 1)
+        opt.step(G, inv_scale=0.25, max_norm=1.0, d_norm=norm, d_found_inf=flag)
+        if k != 1:
+            O = ortho(S, G, M, cfg=cfg, inv_scale=0.25, max_norm=1.0, d_norm=norm)
+            S.hpo_rms_update(O, W2, v, rcfg, workspace(S.hpo_rms_update_workspace(W2)), param=p2.view, scales=s2)
+        for x, y in ((W1, W2), (opt.momentum, M), (opt.v, v), (p1.view, p2.view), (s1, s2)):
+            assert torch.equal(su.bits(x), su.bits(y)), k
+    S.hpo_qk_clip(torch.tensor([90.0, 400.0, 10.0, 100.0], device=DEV), b, 100.0, [opt.clip_weight()])
+    f = torch.tensor([1.0, 0.5, 1.0, 1.0], device=DEV)[:, None, None]
+    assert torch.equal(W1, W2 * f)
+    su.check_weight(W1, p1.view, s1)
+
+
+def test_calls_on_two_streams_at_once(S):
+    """Two stacks worked on by two streams, a workspace each, give what they give alone."""
+    def job(seed, n):
+        W = (0.02 * torch.randn(3, 40, n, generator=gen(seed))).to(DEV)
+        G = gradient(seed + 1, 3, 40, n).to(DEV)
+        return dict(W=W, G=G, O=torch.zeros(3, 40, n, dtype=torch.bfloat16, device=DEV),
+                    v=torch.zeros(3, 40, device=DEV), ws=workspace(S.hpo_orthogonalize_workspace(G)),
+                    ws2=workspace(S.hpo_rms_update_workspace(W)))
+
+    def work(j, times):
+        for _ in range(times):
+            S.hpo_orthogonalize(j["G"], j["O"], S.hpo.make_muon_cfg(), j["ws"])
+            S.hpo_rms_update(j["O"], j["W"], j["v"], S.make_rms_cfg(0.02), j["ws2"])
+
+    alone, both = [job(91, 700), job(93, 300)], [job(91, 700), job(93, 300)]
+    for j in alone:
+        work(j, 5)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for st, j in zip(streams, both):
+        with torch.cuda.stream(st):
+            work(j, 5)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, both):
+        assert torch.equal(su.bits(a["W"]), su.bits(b["W"])) and torch.equal(su.bits(a["O"]), su.bits(b["O"]))
+
+
+def test_offsets_beyond_32_bits(S):
+    """Matrices, heads and rows more than 2^31 elements into their buffer."""
+    far = (1 << 31) + 64
+    buf = torch.zeros(far + 4096, dtype=torch.float32, device=DEV)
+    W = buf.as_strided((2, 8, 32), (far, 32, 1))
+    W0 = 0.02 * torch.randn(2, 8, 32, generator=gen(95))
+    W.copy_(W0)
+    O, v = torch.randn(2, 8, 32, generator=gen(96)), torch.zeros(2, 8)
+    vd = v.to(DEV)
+    S.hpo_rms_update(O.to(DEV), W, vd, S.make_rms_cfg(**CFG), workspace(S.hpo_rms_update_workspace(W)))
+    check_rms(W, vd, W0, O, v, CFG, "far")
+    g = gradient(97, 2, 8, 32)
+    W.copy_(g)
+    check_ortho(ortho(S, W), g.double(), tag="far")
+    big = gradient(98, 2, 140, 24)   # short side over the thin form's with the other orientation below
+    far_rows = buf.as_strided((2, 140, 24), (24, (far - 100) // 140, 1))
+    far_rows.copy_(big)
+    check_ortho(ortho(S, far_rows), big.double(), tag="far rows")
+    W.copy_(W0)
+    S.hpo_qk_clip(torch.tensor([50.0, 400.0], device=DEV), 2, 100.0, [S.ClipWeight(W, 2, 0.5)])
+    assert torch.equal(W.cpu(), W0 * torch.tensor([1.0, 0.5])[:, None, None])
+    del buf, W, far_rows
+    half = torch.zeros(far + 4096, dtype=torch.bfloat16, device=DEV)
+    q, k = (torch.randn(2, 40, 1, 64, generator=gen(n)).bfloat16() for n in (99, 100))
+    qd, kd = half.as_strided((2, 40, 1, 64), (far, 64, 64, 1)), torch.zeros(2, 40, 1, 64, dtype=torch.bfloat16, device=DEV)
+    qd.copy_(q)
+    kd.copy_(k)
+    out = torch.empty(1, device=DEV)
+    for causal in (False, True):
+        S.hpo_qk_max_logits(qd, kd, out, 0.125, causal=causal)
+        check_logits(out, q, k, 0.125, causal, -1, 64, "far queries")
+        S.hpo_qk_max_logits(kd, qd, out, 0.125, causal=causal)
+        check_logits(out, k, q, 0.125, causal, -1, 64, "far keys")
