@@ -77,15 +77,22 @@ typedef struct {
  * have one shape, each its own strides, and do not overlap.  The scale fields
  * of cfg are not read.
  *
- * Arithmetic: the norm in binary64; products on the matrix cores with fp16
- * operands at power-of-two scales that the host derives from the coefficients
- * (a bound on X, A and B at every step), accumulated in fp32; what the
- * rounding of X to fp16 loses is kept beside it for the term a X, so that the
- * small singular values, which grow by a each step, keep their accuracy.  The
- * result is within about 2e-3 (relative, Frobenius) of the exact iteration
- * before its rounding to bf16.  Coefficients whose iteration may leave
- * |X| <= 2^15 for a start of norm 1 are refused (HPO_EINVAL).  A matrix that is all zero
- * gives zeros; one that holds an inf or NaN gives NaN everywhere.
+ * Arithmetic: products on the matrix cores with fp16 operands at power-of-two
+ * scales that the host derives from the coefficients (bounds on X, A and B at
+ * every step), accumulated in fp32.
+ *   Short side over 128: the norm in binary64; what the rounding of X to fp16
+ *     loses is kept beside it for the term a X of every step but the last, so that the small singular
+ *     values, which grow by a each step, keep their accuracy.  Within about
+ *     2e-3 (relative, Frobenius) of the exact iteration before the rounding to
+ *     bf16.
+ *   Short side up to 128 (unless the coefficients' steps multiply to more than
+ *     2^11 in growth): the iteration runs on the Gram matrix of X0 in 22-bit
+ *     products and the long side is touched only at its ends; the norm is the
+ *     root of the Gram matrix's trace.  Within about 5e-4 before the rounding.
+ * Coefficients whose iteration may leave |X| <= 2^15 for a start of norm 1 are
+ * refused (HPO_EINVAL).  A matrix that is all zero gives zeros, as does one whose
+ * norm is beyond fp32's largest value; one that holds an inf or NaN gives NaN everywhere.
+ * The same inputs give the same bits.
  * With a non-zero *d_found_inf (nullable) nothing is written. */
 hpo_status hpo_orthogonalize(const hpo_stack* G, const hpo_stack* momentum, const hpo_stack* out,
                              const hpo_muon_cfg* cfg, float inv_scale, double max_norm, const float* d_norm,
@@ -102,7 +109,7 @@ hpo_status hpo_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols
  *   v_i  = beta2 v_i + (1 - beta2) ms_i       (d_v, fp32 [batch][rows], in place)
  *   r_i  = 1 / (sqrt(v_i) + eps)
  *   N    = sqrt(sum over i of cols * ms_i * r_i^2)   (the norm of the rows r_i O_i)
- *   s    = lr * target_rms * sqrt(rows * cols) / N,  0 where N is 0
+ *   s    = lr * target_rms * sqrt(rows * cols) / N,  0 where N is 0 or not a number
  *   W    = fp32(W * fp32(1 - lr * weight_decay)); W_ij = fp32(W_ij - fp32(s r_i) O_ij)
  * and the model weight, if param is given, takes W rounded to nearest even to
  * bf16, or to HPO_WEIGHT_MX8 with d_scales.  beta2 = 0 is the plain
@@ -110,8 +117,9 @@ hpo_status hpo_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols
  * read, if it is given).  Squares and the mean are summed in fp32 per lane and in
  * binary64 across lanes; N, s and r in binary64.  The sums' order is fixed: the same
  * inputs give the same bits.
- * 0 <= beta2 < 1; eps >= 0, and a row with v_i = 0 is left out of the update;
- * lr, weight_decay and target_rms are finite.
+ * 0 <= beta2 < 1; eps >= 0, and a row with sqrt(v_i) + eps = 0 is left out of the
+ * update; lr, weight_decay and target_rms are finite.  A stack has at most 2^24 rows
+ * in all.
  * With a non-zero *d_found_inf (nullable) nothing is written. */
 typedef struct {
     double lr;
@@ -204,7 +212,8 @@ typedef struct {
  * head whose gamma is under 1: W = fp32(W * f) with f = fp32(gamma^power), and
  * the model weight takes W rounded as in hpo_rms_update.  The rows of the other heads
  * are neither read nor written. With heads == kv_heads both
- * readings are one.  1 <= n_weights <= HPO_CLIP_MAX_WEIGHTS; tau > 0.
+ * readings are one.  1 <= n_weights <= HPO_CLIP_MAX_WEIGHTS; tau > 0.  The weights do
+ * not overlap (views of one buffer are fine); one given twice is refused.
  * With a non-zero *d_found_inf (nullable) nothing is written. */
 hpo_status hpo_qk_clip(const float* d_max, int32_t heads, int32_t kv_heads, double tau, const hpo_clip_weight* weights,
                        int32_t n_weights, const int32_t* d_found_inf, void* stream);

@@ -464,7 +464,9 @@ hpo_status hpo_qk_max_logits(const hpo_qk* a, int32_t accumulate, float* d_max, 
     g.window = a->window < 0 ? -1 : static_cast<int32_t>(std::min<int64_t>(a->window, int64_t{1} << 30));
     g.scale = a->scale;
     g.out = d_max;
-    const int64_t strides[] = {g.qsb, g.qst, g.qsh, g.ksb, g.kst, g.ksh};
+    /* what only one batch row or head would step over does not decide the access width */
+    const int64_t strides[] = {g.batch > 1 ? g.qsb : 0, g.qst, g.heads > 1 ? g.qsh : 0,
+                               g.batch > 1 ? g.ksb : 0, g.kst, g.kv_heads > 1 ? g.ksh : 0};
     bool wide = aligned(a->q, 16) && aligned(a->k, 16);
     for (int64_t s : strides)
         wide = wide && s % 8 == 0;
@@ -510,6 +512,9 @@ hpo_status hpo_qk_clip(const float* d_max, int32_t heads, int32_t kv_heads, doub
             return fail(HPO_EINVAL, "weight %d: per_group must be 0 or 1, reserved 0", k);
         if (is_empty(w.master))
             continue;
+        for (int32_t j = 0; j < a.n; ++j)
+            if (a.item[j].w.master.data == w.master->data)
+                return fail(HPO_EINVAL, "weight %d: the same master is given twice", k);
         hpo::ClipItem& it = a.item[a.n];
         st = weight_view(w.master, w.param, w.d_scales, it.w);
         if (st != HPO_OK)

@@ -100,6 +100,23 @@ def test_orthogonalize(S, b, r, c, dtype):
     check_ortho(out, G.double(), tag=f"{b}x{r}x{c} {dtype}")
 
 
+@pytest.mark.parametrize("b,r,c", [(400, 256, 256), (64, 512, 500), (2, 2048, 2100), (2, 2100, 2048), (1, 4000, 4100),
+                                   (2, 260, 5000), (1, 1300, 9001), (1, 4096, 14336), (1, 14336, 4096), (1, 200, 20000),
+                                   (64, 100, 3000), (300, 3000, 20)])
+def test_orthogonalize_every_tile_and_cut(S, b, r, c):
+    """Stacks that take the larger tiles and the Gram products cut in depth; the reference runs on the GPU."""
+    g = torch.Generator(device=DEV).manual_seed(b + r + c)
+    G = 1e-3 * torch.randn(b, r, c, generator=g, device=DEV)
+    M = 1e-3 * torch.randn(b, r, c, generator=g, device=DEV)
+    gt = G + 0.95 * (0.95 * M + G)
+    out = ortho(S, G, M)
+    for z in sorted({0, b // 2, b - 1}):
+        e, tol = su.ns_tolerance(gt[z])
+        d = float(torch.linalg.vector_norm(out[z].double() - e) / torch.linalg.vector_norm(e))
+        print(f"[ortho] {b}x{r}x{c}[{z}] rel {d:.2e} (allowed {tol:.2e})", flush=True)
+        assert d <= tol, z
+
+
 @pytest.mark.parametrize("layout", ["dense", "padded", "offset", "rows"])
 @pytest.mark.parametrize("r,c", [(100, 333), (260, 130), (64, 256)])
 def test_orthogonalize_strides(S, layout, r, c):
@@ -147,8 +164,9 @@ def test_orthogonalize_low_rank_keeps_its_small_directions(S):
 @pytest.mark.parametrize("steps,coeffs", [(1, None), (2, None), (3, [(8.2, -23.6, 17.3), (4.1, -2.9, 0.5),
                                                                      (1.875, -1.25, 0.375)]),
                                           (4, [(1.5, -0.5, 0.0)] * 4), (1, [(0.0, 0.0, 0.0)]), (7, None)])
-def test_orthogonalize_schedules(S, steps, coeffs):
-    G = gradient(13, 2, 90, 200)
+@pytest.mark.parametrize("r", [90, 150])
+def test_orthogonalize_schedules(S, steps, coeffs, r):
+    G = gradient(13, 2, r, 200)
     cfg = S.hpo.make_muon_cfg(ns_steps=steps, ns_coeffs=coeffs)
     check_ortho(ortho(S, G.to(DEV), cfg=cfg), G.double(), steps, coeffs, tag=f"{steps} steps")
 
@@ -162,8 +180,9 @@ def test_orthogonalize_scale_of_the_input_does_not_matter(S):
         assert torch.equal(su.bits(ortho(S, (G * 2.0 ** e).to(DEV), cfg=cfg)), su.bits(base)), e
 
 
-def test_orthogonalize_zero_and_non_finite(S):
-    G = gradient(19, 4, 40, 60)
+@pytest.mark.parametrize("r,c", [(40, 60), (140, 150)])
+def test_orthogonalize_zero_and_non_finite(S, r, c):
+    G = gradient(19, 4, r, c)
     G[0] = 0.0
     G[1, 3, 5] = math.nan
     G[2, 7, 1] = INF
@@ -737,8 +756,8 @@ def test_offsets_beyond_32_bits(S):
     g = gradient(97, 2, 8, 32)
     W.copy_(g)
     check_ortho(ortho(S, W), g.double(), tag="far")
-    big = gradient(98, 2, 140, 24)   # short side over the thin form's with the other orientation below
-    far_rows = buf.as_strided((2, 140, 24), (24, (far - 100) // 140, 1))
+    big = gradient(98, 2, 140, 150)   # short side over the thin form's
+    far_rows = buf.as_strided((2, 140, 150), (150, (far - 400) // 140, 1))
     far_rows.copy_(big)
     check_ortho(ortho(S, far_rows), big.double(), tag="far rows")
     W.copy_(W0)

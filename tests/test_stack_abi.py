@@ -208,6 +208,7 @@ def test_qk_clip_refusals(S, H):
         (((W, None, None, float("nan"), 0),), {}, "power"),
         (((W, None, None, 0.5, 2),), {}, "per_group"),
         (((None, None, None, 0.5, 0),), {}, "NULL"),
+        (((W, None, None, 0.5, 0), (W, None, None, 1.0, 1)), {}, "twice"),
         (((W, stack(S, dtype=16, batch=4), None, 0.5, 0),), {}, "d_scales"),
         (((W, stack(S, dtype=0, batch=4, cols=9), None, 0.5, 0),), {}, "param is"),
     ]
