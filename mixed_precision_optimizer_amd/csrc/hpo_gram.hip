@@ -133,46 +133,96 @@ struct Raw {
     f32x4_t g[8], m[8];
 };
 
+/* One matrix: a scalar base and 32-bit element offsets (the host sends matrices that
+ * span more than 2^30 elements elsewhere), or the addresses alone would take a
+ * quarter of the registers. */
+struct Mat {
+    const char* g;
+    float* m;
+    uint32_t grs, mrs;
+};
+
+template <bool BF16>
+__device__ __forceinline__ Mat matrix_of(const OrthoSrc& s, int64_t z)
+{
+    Mat x;
+    x.g = static_cast<const char*>(s.G) + z * s.gbs * (BF16 ? 2 : 4);
+    x.m = s.M != nullptr ? s.M + z * s.mbs : nullptr;
+    x.grs = static_cast<uint32_t>(s.grs);
+    x.mrs = static_cast<uint32_t>(s.mrs);
+    return x;
+}
+
+template <bool BF16>
+__device__ __forceinline__ f32x4_t grad_at(const char* base, uint32_t at, int n)
+{
+    f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (BF16) {
+        const char* p = base + at * 2u;
+        if (n >= 4) {
+            const u32x2_t t = *reinterpret_cast<const u32x2_any*>(p);
+            x[0] = bf16_to_f32(t.x & 0xffffu);
+            x[1] = bf16_to_f32(t.x >> 16);
+            x[2] = bf16_to_f32(t.y & 0xffffu);
+            x[3] = bf16_to_f32(t.y >> 16);
+            return x;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n)
+                x[e] = bf16_to_f32(reinterpret_cast<const uint16_t*>(p)[e]);
+    } else {
+        const char* p = base + at * 4u;
+        if (n >= 4)
+            return *reinterpret_cast<const f32x4_any*>(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e < n)
+                x[e] = reinterpret_cast<const float*>(p)[e];
+    }
+    return x;
+}
+
 /* A share's elements in memory: LDS row = short side (GRAM) or long side
  * (apply), columns of the wide form from k0 on. */
 template <bool TALL, bool GRAM, int LROW, int LCOL>
-__device__ __forceinline__ void place(const OrthoSrc& s, int64_t k0, int j, int64_t& row, int64_t& col, int& cnt)
+__device__ __forceinline__ void place(const OrthoSrc& s, int64_t k0, int j, uint32_t& row, uint32_t& col, int& cnt)
 {
     int r, c;
     Share<LROW, LCOL, GRAM != TALL>::run(j, r, c);
-    const int64_t i = GRAM ? r : c, kk = k0 + (GRAM ? c : r);   /* short, long coordinate */
-    row = TALL ? kk : i;
-    col = TALL ? i : kk;
-    const int64_t left = row < s.rows ? s.cols - col : 0;
-    cnt = left >= 4 ? 4 : (left > 0 ? static_cast<int>(left) : 0);
+    const int i = GRAM ? r : c, kk = static_cast<int>(k0) + (GRAM ? c : r);   /* short, long coordinate */
+    const int y = TALL ? kk : i, x = TALL ? i : kk;
+    row = static_cast<uint32_t>(y);
+    col = static_cast<uint32_t>(x);
+    const int left = y < static_cast<int>(s.rows) ? static_cast<int>(s.cols) - x : 0;
+    cnt = left >= 4 ? 4 : (left > 0 ? left : 0);
 }
 
 template <bool BF16, bool TALL, bool GRAM, int LROW, int LCOL>
-__device__ __forceinline__ void fetch(const GramArgs& a, int64_t z, int64_t k0, Raw& x)
+__device__ __forceinline__ void fetch(const GramArgs& a, const Mat& t, int64_t k0, Raw& x)
 {
-    const OrthoSrc& s = a.s;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        int64_t row, col;
+        uint32_t row, col;
         int cnt;
-        place<TALL, GRAM, LROW, LCOL>(s, k0, j, row, col, cnt);
-        x.g[j] = grad4<BF16>(s, z * s.gbs + row * s.grs + col, cnt);
-        if (s.M != nullptr)
-            x.m[j] = momentum4(s, z * s.mbs + row * s.mrs + col, cnt);
+        place<TALL, GRAM, LROW, LCOL>(a.s, k0, j, row, col, cnt);
+        x.g[j] = grad_at<BF16>(t.g, row * t.grs + col, cnt);
+        if (t.m != nullptr)
+            x.m[j] = grad_at<false>(reinterpret_cast<const char*>(t.m), row * t.mrs + col, cnt);
     }
 }
 
 /* g~ of a fetched share in x.g.  The first pass (GRAM) updates the momentum in
  * memory; the second reads it as it is after the update. */
 template <bool TALL, bool GRAM, int LROW, int LCOL>
-__device__ __forceinline__ void finish(const GramArgs& a, const GradVals& k, int64_t z, int64_t k0, Raw& x)
+__device__ __forceinline__ void finish(const GramArgs& a, const Mat& t, const GradVals& k, int64_t k0, Raw& x)
 {
-    const OrthoSrc& s = a.s;
+    const MuonScalars& sc = a.s.sc;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        int64_t row, col;
+        uint32_t row, col;
         int cnt;
-        place<TALL, GRAM, LROW, LCOL>(s, k0, j, row, col, cnt);
+        place<TALL, GRAM, LROW, LCOL>(a.s, k0, j, row, col, cnt);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float g = x.g[j][e] * k.inv_scale;
@@ -180,17 +230,25 @@ __device__ __forceinline__ void finish(const GramArgs& a, const GradVals& k, int
                 g = g * k.C;
             x.g[j][e] = g;
         }
-        if (s.M != nullptr) {
+        if (t.m != nullptr) {
             if constexpr (GRAM) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    x.m[j][e] = s.sc.form == HPO_MUON_MOMENTUM_SUM ? s.sc.mu * x.m[j][e] + x.g[j][e]
-                                                                    : s.sc.mu * x.m[j][e] + s.sc.omu * x.g[j][e];
-                put_momentum4(s, z * s.mbs + row * s.mrs + col, cnt, x.m[j]);
+                    x.m[j][e] = sc.form == HPO_MUON_MOMENTUM_SUM ? sc.mu * x.m[j][e] + x.g[j][e]
+                                                                  : sc.mu * x.m[j][e] + sc.omu * x.g[j][e];
+                char* p = reinterpret_cast<char*>(t.m) + (row * t.mrs + col) * 4u;
+                if (cnt >= 4) {
+                    *reinterpret_cast<f32x4_any*>(p) = x.m[j];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (e < cnt)
+                            reinterpret_cast<float*>(p)[e] = x.m[j][e];
+                }
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                x.g[j][e] = nesterov_of(x.g[j][e], x.m[j][e], s.sc);
+                x.g[j][e] = nesterov_of(x.g[j][e], x.m[j][e], sc);
         }
         /* behind the edge 0 * C is 0 or, with a clip that is not a number, not one: edges are zeros */
 #pragma unroll
@@ -266,10 +324,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram(GramArgs a)
             acc[i][j] = f32x16_t{};
     int top = -1000;   /* the sums are scaled by 2^(2 (kTop - top)) */
     using Sh = Share<MP, KC, !TALL>;
+    const Mat mat = matrix_of<BF16>(a.s, z);
     Raw x;
-    fetch<BF16, TALL, true, MP, KC>(a, z, c0, x);
+    fetch<BF16, TALL, true, MP, KC>(a, mat, c0, x);
     for (int64_t k0 = c0; k0 < c1; k0 += KC) {
-        finish<TALL, true, MP, KC>(a, gv, z, k0, x);
+        finish<TALL, true, MP, KC>(a, mat, gv, k0, x);
         const f32x4_t(&v)[8] = x.g;
         uint32_t m = 0;
 #pragma unroll
@@ -327,7 +386,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram(GramArgs a)
         }
         __syncthreads();
         if (k0 + KC < c1)   /* the next tile arrives under this one's products */
-            fetch<BF16, TALL, true, MP, KC>(a, z, k0 + KC, x);
+            fetch<BF16, TALL, true, MP, KC>(a, mat, k0 + KC, x);
 #pragma unroll
         for (int s = 0; s < kSlices; ++s) {
             u32x4_t fa[kB], fb[kB], fl[kB];
@@ -665,10 +724,11 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram_apply(GramArgs a)
         pl[s] = *reinterpret_cast<const u32x4_t*>(P + MP * MP + at);
     }
     using Sh = Share<KC, MP, TALL>;
+    const Mat mat = matrix_of<BF16>(a.s, z);
     Raw x;
-    fetch<BF16, TALL, false, KC, MP>(a, z, c0, x);
+    fetch<BF16, TALL, false, KC, MP>(a, mat, c0, x);
     for (int64_t k0 = c0; k0 < c1; k0 += KC) {
-        finish<TALL, false, KC, MP>(a, gv, z, k0, x);
+        finish<TALL, false, KC, MP>(a, mat, gv, k0, x);
         const f32x4_t(&v)[8] = x.g;
         __syncthreads();   /* the previous tile's fragments are read */
 #pragma unroll
@@ -687,7 +747,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram_apply(GramArgs a)
         }
         __syncthreads();
         if (k0 + KC < c1)
-            fetch<BF16, TALL, false, KC, MP>(a, z, k0 + KC, x);
+            fetch<BF16, TALL, false, KC, MP>(a, mat, k0 + KC, x);
         f32x16_t acc[2] = {f32x16_t{}, f32x16_t{}};
 #pragma unroll
         for (int s = 0; s < kSlices; ++s) {
@@ -707,16 +767,20 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram_apply(GramArgs a)
             }
         }
         const int down = -(a.p_exp + kTop);
+        char* out = reinterpret_cast<char*>(a.out + z * a.obs);
+        const uint32_t ors = static_cast<uint32_t>(a.ors);
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const int reg = 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-                const int64_t i = i0 + (TALL ? lane & 31 : reg);
-                const int64_t kk = k0 + j0 + 32 * j + (TALL ? reg : lane & 31);
-                if (i < a.m && kk < a.n)
-                    a.out[z * a.obs + (TALL ? kk * a.ors + i : i * a.ors + kk)] =
+                const int i = i0 + (TALL ? lane & 31 : reg);
+                const int kk = static_cast<int>(k0) + j0 + 32 * j + (TALL ? reg : lane & 31);
+                if (i < static_cast<int>(a.m) && kk < static_cast<int>(a.n)) {
+                    const uint32_t at = TALL ? static_cast<uint32_t>(kk) * ors + i : static_cast<uint32_t>(i) * ors + kk;
+                    *reinterpret_cast<uint16_t*>(out + at * 2u) =
                         static_cast<uint16_t>(bf16_rne_bits(__builtin_ldexpf(acc[j][r], down)));
+                }
             }
     }
 }

@@ -388,6 +388,7 @@ __global__ __launch_bounds__(kRowThreads) void k_rms_apply(RmsArgs a)
 /* ---------------------------------------------------------------------- */
 /* hpo_qk_clip                                                             */
 /* ---------------------------------------------------------------------- */
+template <bool NT>
 __global__ __launch_bounds__(kRowThreads) void k_qk_clip(ClipArgs a)
 {
     if (skipped(a.d_found))
@@ -422,9 +423,9 @@ __global__ __launch_bounds__(kRowThreads) void k_qk_clip(ClipArgs a)
         f32x4_t x[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-            x[u] = load4(static_cast<const float*>(wv.master.data) + z * wv.master.bs + p[u].row * wv.master.rs +
-                             p[u].col,
-                         p[u].n);
+            x[u] = load4<NT>(static_cast<const float*>(wv.master.data) + z * wv.master.bs + p[u].row * wv.master.rs +
+                                 p[u].col,
+                             p[u].n);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
             if (u >= n)
@@ -432,12 +433,12 @@ __global__ __launch_bounds__(kRowThreads) void k_qk_clip(ClipArgs a)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 x[u][e] = x[u][e] * f;
-            store4(static_cast<float*>(wv.master.data) + z * wv.master.bs + p[u].row * wv.master.rs + p[u].col, x[u],
-                   p[u].n);
+            store4<NT>(static_cast<float*>(wv.master.data) + z * wv.master.bs + p[u].row * wv.master.rs + p[u].col, x[u],
+                       p[u].n);
             if (wv.param_dtype == HPO_PARAM_BF16)
-                store_weight<HPO_PARAM_BF16>(wv, z, p[u], x[u]);
+                store_weight<HPO_PARAM_BF16, NT>(wv, z, p[u], x[u]);
             else if (wv.param_dtype == HPO_WEIGHT_MX8)
-                store_weight<HPO_WEIGHT_MX8>(wv, z, p[u], x[u]);
+                store_weight<HPO_WEIGHT_MX8, NT>(wv, z, p[u], x[u]);
         }
     });
 }
@@ -466,6 +467,14 @@ int64_t blocks_of(const WeightView& w, int64_t run)
     return (w.rows * pieces + kRowWaves * run - 1) / (kRowWaves * run);
 }
 
+/* Bytes of master and model weight per element (8-bit scales left out). */
+int64_t bytes_of(const WeightView& w)
+{
+    return w.param_dtype == HPO_PARAM_FP32 ? 4 : (w.param_dtype == HPO_PARAM_BF16 ? 6 : 5);
+}
+
+constexpr int64_t kStreamBytes = int64_t{64} << 20;
+
 template <typename OT>
 hipError_t rms_update(RmsArgs a, hipStream_t stream)
 {
@@ -484,10 +493,11 @@ hipError_t rms_update(RmsArgs a, hipStream_t stream)
     constexpr int32_t kRounds = 4;
     a.rounds = small ? 1 : kRounds;
     const dim3 grid(static_cast<uint32_t>(blocks_of(a.w, small ? 1 : kRounds * kUnroll)), static_cast<uint32_t>(a.batch));
-    /* Masters and weights beyond the on-die cache go around it, which leaves it to O between the two
-     * passes: 4096 x 14336 takes 135 us so and 165 us through the caches, 4 x 2048 x 2048 47 us and 42 us. */
-    const int64_t bytes = a.batch * rows * a.w.cols * (a.w.param_dtype == HPO_PARAM_FP32 ? 4 : (a.w.param_dtype == HPO_PARAM_BF16 ? 6 : 5));
-    const bool nt = bytes > kCachedMaxBytes;
+    /* Larger masters and weights go around the caches, which leaves these to O between the two passes:
+     * 4096 x 14336 takes 135 us so and 165 us through them; with other states in between (as in a step
+     * over a whole model) 16 x 1024 x 2048 takes 77 and 90 us, half of it 44 and 49, a quarter 26 and
+     * 25; a lone state that stays in the cache loses 2 %. */
+    const bool nt = a.batch * rows * a.w.cols * bytes_of(a.w) > kStreamBytes;
     /* every workgroup sums the parts itself (and one launch is saved) unless they are very many */
     constexpr int64_t kFoldParts = 1024;
     const bool fold = a.parts > kFoldParts;
@@ -514,9 +524,12 @@ hipError_t launch_rms_update(const RmsArgs& a, hipStream_t stream)
 
 hipError_t launch_qk_clip(ClipArgs& a, hipStream_t stream)
 {
-    int64_t total = 0;
-    for (int32_t k = 0; k < a.n; ++k)
-        total += static_cast<int64_t>(a.item[k].heads) * blocks_of(a.item[k].w, kUnroll);
+    int64_t total = 0, bytes = 0;
+    for (int32_t k = 0; k < a.n; ++k) {
+        const ClipItem& it = a.item[k];
+        total += it.heads * blocks_of(it.w, kUnroll);
+        bytes += it.heads * it.w.rows * it.w.cols * bytes_of(it.w);
+    }
     /* most workgroups of a wide layer only find that their head is not clipped: above 4096 of them,
      * longer runs */
     const int32_t rounds = static_cast<int32_t>(std::min<int64_t>(4, (total + 4095) / 4096));
@@ -529,7 +542,9 @@ hipError_t launch_qk_clip(ClipArgs& a, hipStream_t stream)
     }
     if (total == 0)
         return hipSuccess;
-    return launch(k_qk_clip, dim3(static_cast<uint32_t>(total)), kRowThreads, stream, a);
+    const dim3 grid(static_cast<uint32_t>(total));
+    return bytes > kStreamBytes ? launch(k_qk_clip<true>, grid, kRowThreads, stream, a)
+                                : launch(k_qk_clip<false>, grid, kRowThreads, stream, a);
 }
 
 }  // namespace hpo

@@ -334,7 +334,9 @@ hpo_status hpo_orthogonalize(const hpo_stack* G, const hpo_stack* momentum, cons
     a.M = view(momentum);
     a.out = view(out);
     a.g_bf16 = G->dtype == HPO_PARAM_BF16 ? 1 : 0;
-    a.use_gram = a.use_gram && std::min(G->rows, G->cols) <= hpo::kGramMax ? 1 : 0;
+    /* the thin form addresses a matrix with 32-bit offsets */
+    auto near = [](const hpo_stack* s) { return !s || (s->rows - 1) * s->row_stride + s->cols <= int64_t{1} << 30; };
+    a.use_gram = a.use_gram && std::min(G->rows, G->cols) <= hpo::kGramMax && near(G) && near(momentum) && near(out);
     a.batch = G->batch;
     a.rows = G->rows;
     a.cols = G->cols;
