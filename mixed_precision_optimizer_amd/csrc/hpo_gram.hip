@@ -294,25 +294,22 @@ __device__ __forceinline__ int part_at(int bi, int bj, int q, int lane)
 /* ---------------------------------------------------------------------- */
 /* S in parts                                                              */
 /* ---------------------------------------------------------------------- */
-/* grid (chunks, batch).  LDS: h and 2 l of an [MP][KC] tile.  MP = 128, 64:
+/* One workgroup's run of columns (c0 .. c1 - 1).  LDS: h and 2 l of an [MP][KC] tile.  MP = 128, 64:
  * 2 x 2 wavefronts over the MP x MP result; MP = 32: every wavefront takes a
  * quarter of the tile's columns for the whole result. */
+constexpr int kTileBytes = 2 * kTileElems * 2;   /* both halves of a column tile */
+
 template <bool BF16, int MP, bool TALL>
-__global__ __launch_bounds__(kThreads, 2) void k_gram(GramArgs a)
+__device__ __forceinline__ void gram_part(const GramArgs& a, int64_t z, int64_t chunk, char* lds, uint32_t* wave_top)
 {
-    if (!gate_open(a.s.sc.gate))
-        return;
     constexpr int KC = kTileElems / MP;
     constexpr int kBytes = kTileElems * 2;
     constexpr int kB = MP == 128 ? 2 : 1;               /* 32 x 32 blocks per wavefront and side */
     constexpr bool kSplitK = MP == 32;
     constexpr int kSlices = KC / 16 / (kSplitK ? 4 : 1);
-    __shared__ __attribute__((aligned(16))) char lds[2 * kBytes];
-    __shared__ uint32_t wave_top[4];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const GradVals gv = grad_vals(a.s.sc);
-    const int64_t z = blockIdx.y;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.run;
+    const int64_t c0 = chunk * a.run;
     const int64_t c1 = c0 + a.run < a.n ? c0 + a.run : a.n;
     const int r0 = kSplitK ? 0 : (wave >> 1) * 32 * kB, q0 = kSplitK ? 0 : (wave & 1) * 32 * kB;
     const int s0 = kSplitK ? wave * kSlices : 0;
@@ -405,9 +402,9 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram(GramArgs a)
                 }
         }
     }
-    float* out = a.part + (z * a.chunks + blockIdx.x) * (MP * MP);
+    float* out = a.part + (z * a.chunks + chunk) * (MP * MP);
     if (tid == 0)
-        a.part_exp[z * a.chunks + blockIdx.x] = top;
+        a.part_exp[z * a.chunks + chunk] = top;
     /* in the order of the registers that the next kernel sums them in: four rows of one column
      * a lane, 1 KB an access */
     if constexpr (kSplitK) {
@@ -440,6 +437,17 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram(GramArgs a)
                     reinterpret_cast<f32x4_t*>(out)[part_at<MP>(r0 / 32 + i, q0 / 32 + j, q, lane)] = t;
                 }
     }
+}
+
+/* grid (chunks, batch) */
+template <bool BF16, int MP, bool TALL>
+__global__ __launch_bounds__(kThreads, 2) void k_gram(GramArgs a)
+{
+    if (!gate_open(a.s.sc.gate))
+        return;
+    __shared__ __attribute__((aligned(16))) char lds[kTileBytes];
+    __shared__ uint32_t wave_top[4];
+    gram_part<BF16, MP, TALL>(a, blockIdx.y, blockIdx.x, lds, wave_top);
 }
 
 /* Sums the parts of S where they are many: a workgroup takes 1024 of each matrix's values
@@ -485,22 +493,21 @@ struct Iter {
     static constexpr int WM = MP / 32, WN = MP == 32 ? 1 : 2;
     static constexpr int BN = MP / 32 / WN;   /* blocks of a wavefront: one row, BN columns */
     static constexpr int kThreads = 64 * WM * WN;
+    static constexpr int kMatBytes = 2 * 2 * 2 * MP * MP, kRawBytes = MP * (MP + 1) * 4;
+    static constexpr int kLds = kMatBytes > kRawBytes ? kMatBytes : kRawBytes;
 };
 
 __device__ __forceinline__ float pow2f(int e) { return __builtin_ldexpf(1.0f, e); }
 
+/* `wave`: the wavefront's place; wavefronts that share one do the same work and store the
+ * same values. */
 template <int MP>
-__global__ __launch_bounds__(Iter<MP>::kThreads) void k_gram_iterate(GramArgs a)
+__device__ __forceinline__ void iterate(const GramArgs& a, int64_t z, int wave, char* lds)
 {
-    if (!gate_open(a.s.sc.gate))
-        return;
     constexpr int WN = Iter<MP>::WN, BN = Iter<MP>::BN;
     constexpr int kPlane = MP * MP * 2, kBuf = 2 * kPlane;
-    constexpr int kRaw = MP * (MP + 1) * 4;
-    __shared__ __attribute__((aligned(16))) char lds[2 * kBuf > kRaw ? 2 * kBuf : kRaw];
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int r0 = (wave / WN) * 32, q0 = (wave % WN) * 32 * BN;
-    const int64_t z = blockIdx.x;
     typedef f32x16_t Block[BN];
     const int lrow = r0 + 4 * (lane >> 5), lcol = q0 + (lane & 31);
     auto row_of = [&](int r) { return lrow + 8 * (r >> 2) + (r & 3); };
@@ -690,27 +697,32 @@ __global__ __launch_bounds__(Iter<MP>::kThreads) void k_gram_iterate(GramArgs a)
         }
 }
 
+template <int MP>
+__global__ __launch_bounds__(Iter<MP>::kThreads) void k_gram_iterate(GramArgs a)
+{
+    if (!gate_open(a.s.sc.gate))
+        return;
+    __shared__ __attribute__((aligned(16))) char lds[Iter<MP>::kLds];
+    iterate<MP>(a, blockIdx.x, threadIdx.x >> 6, lds);
+}
+
 /* ---------------------------------------------------------------------- */
 /* O = P X0                                                                */
 /* ---------------------------------------------------------------------- */
-/* grid (chunks, batch).  LDS: h and l of a [KC][MP] tile (X0's columns).  Each
+/* One workgroup's run of columns.  LDS: h and l of a [KC][MP] tile (X0's columns).  Each
  * wavefront takes 32 rows of P (its fragments in registers) and two blocks of 32
  * columns; the result of a tall matrix comes out transposed, so that lanes always
  * run along its rows. */
 template <bool BF16, int MP, bool TALL>
-__global__ __launch_bounds__(kThreads, 2) void k_gram_apply(GramArgs a)
+__device__ __forceinline__ void apply(const GramArgs& a, int64_t z, int64_t chunk, char* lds)
 {
-    if (!gate_open(a.s.sc.gate))
-        return;
     constexpr int KC = kTileElems / MP;
     constexpr int kBytes = kTileElems * 2;
     constexpr int kSlices = MP / 16;
     constexpr int kRowBlocks = MP / 32;
-    __shared__ __attribute__((aligned(16))) char lds[2 * kBytes];
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     const GradVals gv = grad_vals(a.s.sc);
-    const int64_t z = blockIdx.y;
-    const int64_t c0 = static_cast<int64_t>(blockIdx.x) * a.run;
+    const int64_t c0 = chunk * a.run;
     const int64_t c1 = c0 + a.run < a.n ? c0 + a.run : a.n;
     const float mant = a.inv[2 * z];
     const int ex = static_cast<int>(a.inv[2 * z + 1]);
@@ -785,6 +797,34 @@ __global__ __launch_bounds__(kThreads, 2) void k_gram_apply(GramArgs a)
     }
 }
 
+/* grid (chunks, batch) */
+template <bool BF16, int MP, bool TALL>
+__global__ __launch_bounds__(kThreads, 2) void k_gram_apply(GramArgs a)
+{
+    if (!gate_open(a.s.sc.gate))
+        return;
+    __shared__ __attribute__((aligned(16))) char lds[kTileBytes];
+    apply<BF16, MP, TALL>(a, blockIdx.y, blockIdx.x, lds);
+}
+
+/* All three where one workgroup takes a whole matrix (grid: batch): what a
+ * workgroup wrote to its own scratch it reads behind a barrier. */
+template <bool BF16, int MP, bool TALL>
+__global__ __launch_bounds__(kThreads, 2) void k_gram_whole(GramArgs a)
+{
+    if (!gate_open(a.s.sc.gate))
+        return;
+    static_assert(Iter<MP>::kLds <= kTileBytes && Iter<MP>::kThreads <= kThreads, "the steps fit the tile's LDS");
+    __shared__ __attribute__((aligned(16))) char lds[kTileBytes];
+    __shared__ uint32_t wave_top[4];
+    const int64_t z = blockIdx.x;
+    gram_part<BF16, MP, TALL>(a, z, 0, lds, wave_top);
+    __syncthreads();
+    iterate<MP>(a, z, (threadIdx.x >> 6) % (Iter<MP>::kThreads / 64), lds);
+    __syncthreads();
+    apply<BF16, MP, TALL>(a, z, 0, lds);
+}
+
 template <typename... Args>
 hipError_t launch(void (*kernel)(Args...), dim3 grid, int block, hipStream_t stream, Args... args)
 {
@@ -824,6 +864,10 @@ GramPlan gram_plan(int64_t batch, int64_t rows, int64_t cols)
 template <bool BF16, int MP, bool TALL>
 hipError_t run(const GramArgs& a, uint32_t count, hipStream_t stream)
 {
+    if constexpr (MP <= 64) {
+        if (a.chunks == 1)
+            return launch(k_gram_whole<BF16, MP, TALL>, dim3(count), kThreads, stream, a);
+    }
     const dim3 grid(static_cast<uint32_t>(a.chunks), count);
     hipError_t e = launch(k_gram<BF16, MP, TALL>, grid, kThreads, stream, a);
     if (e != hipSuccess)
