@@ -69,15 +69,16 @@ __device__ __forceinline__ f32x16_t mfma(u32x4_t a, u32x4_t b, f32x16_t c)
 }
 
 /* Byte offset of 16-byte piece p of an LDS row of ROW elements, the pieces
- * permuted by the row so that a fragment's 16 rows meet distinct banks. */
+ * permuted by the row so that a fragment's 16 rows meet distinct banks; the row's higher
+ * bits spread the writes of every fourth row that a tile laid across memory makes. */
 template <int ROW>
 __device__ __forceinline__ int piece_at(int r, int p)
 {
     int f;
     if constexpr (ROW >= 128)
-        f = r & 15;
+        f = (r & 15) ^ ((r >> 4) & 3);
     else if constexpr (ROW == 64)
-        f = (r & 7) ^ ((r >> 3) & 1);
+        f = (r & 7) ^ ((r >> 3) & 1) ^ ((r >> 3) & 2);
     else
         f = (r ^ (r >> 2)) & 3;
     return r * (ROW * 2) + ((p ^ f) << 4);
