@@ -1,7 +1,9 @@
 /*
  * hpo_muon.hip -- gfx950 kernels of the Muon step: momentum and Nesterov
  * gradient, Newton-Schulz orthogonalization on the bf16 matrix cores, and
- * the decayed, scaled master update with the 16-bit write-back.
+ * the decayed, scaled master update with the 16-bit write-back.  The same
+ * GEMMs with fp16 operands and smaller tiles serve hpo_orthogonalize's stacks
+ * (their section is at the end).
  *
  * Sources (web pages):
  *   [HANDBOOK]   "优化器：AdamW、Muon 与分布式优化器" (ai-infra-handbooks,
@@ -1338,6 +1340,15 @@ hipError_t ns_step(const TensorDesc* d_desc, const MuonInfo* d_info, const MuonB
 /* ---------------------------------------------------------------------- */
 /* the stack's iteration (hpo_orthogonalize)                               */
 /* ---------------------------------------------------------------------- */
+/* The GEMMs above with fp16 operands (eight times finer than bf16 at the same
+ * rate) and what the rounding of X loses beside it for the residual a X: a first rounding
+ * of X is amplified by a^5 in the directions of the small singular values, which costs 3e-2
+ * of the result for a low rank over 1 % of noise with either operand alone and 4e-4 with
+ * both.  (Matrices with a short side up to 128 take hpo_gram.hip instead.)
+ * Bound by the matrix cores at the clock they leave themselves; measured on 4096 x 14336
+ * (4.33 ms in all): norm 57 us and input 95 us (HBM), Gram 247 us in three parts of its depth +
+ * 33 us for their sum, A A^T 97 us, step 505 us (its epilogue moves 10 bytes per element), last
+ * step 457 us.  3 x 1000 x 333: 17 launches of 6 to 9 us, 139 us. */
 constexpr int kSumThreads = 512;
 constexpr int64_t kSumMax = 512;      /* partial sums of squares per matrix, at most */
 constexpr int64_t kSumPer = 8192;     /* elements a workgroup sums at the least */
