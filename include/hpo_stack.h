@@ -119,7 +119,7 @@ hpo_status hpo_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols
  * inputs give the same bits.
  * 0 <= beta2 < 1; eps >= 0, and a row with sqrt(v_i) + eps = 0 is left out of the
  * update; lr, weight_decay and target_rms are finite.  A stack has at most 2^24 rows
- * in all.
+ * in all.  O, the master, the model weight, d_scales and d_v do not overlap.
  * With a non-zero *d_found_inf (nullable) nothing is written. */
 typedef struct {
     double lr;
@@ -183,8 +183,8 @@ typedef struct {
  * pairs that head h sees, in every sequence ([OPT-INFRA] §6: S_max^h); products
  * exact, sums in fp32 on the matrix cores.  -inf where no pair is seen; NaN if
  * a seen logit is NaN (values behind the mask or behind a sequence's end never
- * count).  accumulate = 1 takes the larger of that and d_max[h] as it is: the
- * maximum over micro-batches.  The result does not depend on the order of the
+ * count).  accumulate = 1 takes the larger of that and d_max[h] as it is (NaN if
+ * either is): the maximum over micro-batches.  The result does not depend on the order of the
  * work. */
 hpo_status hpo_qk_max_logits(const hpo_qk* a, int32_t accumulate, float* d_max, void* stream);
 

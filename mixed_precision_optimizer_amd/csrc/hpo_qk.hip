@@ -343,15 +343,19 @@ __global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a)
         /* rounding is monotone: the largest product times scale is the largest logit.  Adding 0
          * turns -0 into 0.  As bits, non-negative values (and the positive NaN above
          * them) order as signed integers, negative ones fall as unsigned grow; each atomic
-         * only ever raises the value, so their order does not matter. */
+         * only ever raises the value, so their order does not matter.  A NaN of the caller's with
+         * its sign set lies below everything: whoever replaces it puts a NaN back. */
         const float v = best * a.scale + 0.0f;
         float* out = a.out + h;
+        uint32_t before = 0;
         if (v != v)
             atomicMax(reinterpret_cast<int*>(out), 0x7fc00000);
         else if (v >= 0.0f)
-            atomicMax(reinterpret_cast<int*>(out), __float_as_int(v));
+            before = static_cast<uint32_t>(atomicMax(reinterpret_cast<int*>(out), __float_as_int(v)));
         else if (v > -INFINITY)
-            atomicMin(reinterpret_cast<unsigned int*>(out), __float_as_uint(v));
+            before = atomicMin(reinterpret_cast<unsigned int*>(out), __float_as_uint(v));
+        if (a.accumulate && before > 0xff800000u)
+            atomicMax(reinterpret_cast<int*>(out), 0x7fc00000);
     }
 }
 
@@ -393,9 +397,9 @@ hipError_t launch_type(const QkArgs& a, bool aligned, uint32_t grid, hipStream_t
 
 }  // namespace
 
-hipError_t launch_qk_max(QkArgs a, bool fp16, bool aligned, bool accumulate, hipStream_t stream)
+hipError_t launch_qk_max(QkArgs a, bool fp16, bool aligned, hipStream_t stream)
 {
-    if (!accumulate) {
+    if (!a.accumulate) {
         hipError_t e = launch(k_fill, dim3((a.heads + 255) / 256), 256, stream, a.out, static_cast<int>(a.heads), -INFINITY);
         if (e != hipSuccess)
             return e;

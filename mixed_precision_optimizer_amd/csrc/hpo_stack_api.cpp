@@ -464,6 +464,7 @@ hpo_status hpo_qk_max_logits(const hpo_qk* a, int32_t accumulate, float* d_max, 
     g.max_k = static_cast<int32_t>(packed ? std::max<int64_t>(1, std::min(a->max_seqlen_k, a->seq_k)) : a->seq_k);
     g.causal = a->causal;
     g.window = a->window < 0 ? -1 : static_cast<int32_t>(std::min<int64_t>(a->window, int64_t{1} << 30));
+    g.accumulate = accumulate;
     g.scale = a->scale;
     g.out = d_max;
     /* what only one batch row or head would step over does not decide the access width */
@@ -477,7 +478,7 @@ hpo_status hpo_qk_max_logits(const hpo_qk* a, int32_t accumulate, float* d_max, 
         if (tiles > (int64_t{1} << 23))
             return fail(HPO_EINVAL, "%lld query tiles are more than one launch can hold", (long long)tiles);
     }
-    const hipError_t e = hpo::launch_qk_max(g, a->dtype == HPO_PARAM_FP16, wide, accumulate != 0, as_stream(stream));
+    const hipError_t e = hpo::launch_qk_max(g, a->dtype == HPO_PARAM_FP16, wide, as_stream(stream));
     if (e != hipSuccess)
         return hip_fail(e, "launch attention logit maxima");
     return ok();

@@ -84,11 +84,12 @@ struct QkArgs {
     int32_t max_q, max_k;      /* lengths the launch is sized for */
     int32_t causal, window;    /* window < 0: none */
     int32_t q_tiles, splits;
+    int32_t accumulate;        /* out holds values of the caller's */
     float scale;
     float* out;
 };
 
-hipError_t launch_qk_max(QkArgs a, bool fp16, bool aligned, bool accumulate, hipStream_t stream);
+hipError_t launch_qk_max(QkArgs a, bool fp16, bool aligned, hipStream_t stream);
 
 /* ---------------------------------------------------------------------- */
 /* Newton-Schulz of a stack                                                */

@@ -194,7 +194,7 @@ class StackMuon:
              d_norm=None, d_found_inf=None) -> None:
         """One step from the stored grad (fp32 or bf16, master's shape).  inv_scale,
         the clip by d_norm and the skip on d_found_inf are the chain's, as in
-        hpo_muon_step; a skipped step changes nothing."""
+        hpo_muon_step; a skipped step changes nothing.  An lr given here stays."""
         if lr is not None:
             self.rms.lr = lr
         hpo_stack.hpo_orthogonalize(grad, self.update, self.muon, self._ws, self.momentum, inv_scale, max_norm, d_norm,
@@ -203,5 +203,6 @@ class StackMuon:
                                  d_found_inf)
 
     def clip_weight(self, power: float = 0.5, per_group: bool = True) -> hpo_stack.ClipWeight:
-        """This weight for hpo_qk_clip, one matrix of the stack per head."""
-        return hpo_stack.ClipWeight(self.master, self.master.shape[0], power, self.param, self.scales, per_group)
+        """This weight for hpo_qk_clip, one matrix of the stack per head (a lone matrix is one head)."""
+        heads = self.master.shape[0] if self.master.dim() == 3 else 1
+        return hpo_stack.ClipWeight(self.master, heads, power, self.param, self.scales, per_group)

@@ -775,3 +775,23 @@ def test_offsets_beyond_32_bits(S):
         check_logits(out, q, k, 0.125, causal, -1, 64, "far queries")
         S.hpo_qk_max_logits(kd, qd, out, 0.125, causal=causal)
         check_logits(out, k, q, 0.125, causal, -1, 64, "far keys")
+
+
+@pytest.mark.parametrize("value", [1.0, -1.0])
+def test_qk_max_keeps_a_nan_of_either_sign_when_it_accumulates(S, value):
+    """A NaN already in d_max stays one, whatever its sign bit and the sign of the new maxima."""
+    q = torch.ones(2, 300, 3, 64, dtype=torch.bfloat16, device=DEV)
+    k = value * torch.ones_like(q)
+    for pattern in (0x7FC00000, 0xFFC00000 - (1 << 32), 0xFF800001 - (1 << 32)):
+        o = torch.full((3,), pattern, dtype=torch.int32, device=DEV).view(torch.float32)
+        S.hpo_qk_max_logits(q, k, o, 0.125, causal=False, accumulate=True)
+        assert bool(o.isnan().all()), hex(pattern)
+
+
+def test_stack_muon_of_one_matrix_clips_as_one_head(S):
+    from mixed_precision_optimizer_amd import StackMuon
+    W = torch.randn(6, 40, generator=gen(91)).to(DEV)
+    before = W.clone()
+    opt = StackMuon(W, lr=0.02)
+    S.hpo_qk_clip(torch.tensor([400.0], device=DEV), 1, 100.0, [opt.clip_weight()])
+    assert torch.equal(W, before * 0.5)
