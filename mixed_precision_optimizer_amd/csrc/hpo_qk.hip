@@ -16,12 +16,12 @@
  * each lane keeps one number, folded with v_maximum3 (two logits an
  * instruction, NaN stays NaN).
  *
- * Measured: 8192 causal tokens, 32 heads over 8, dim 128, bf16: 206 us, 1.33
- * PFLOP/s of the seen pairs (a large library product reaches 1.20 here); the matrix
- * cores are busy 65 % of the cycles at the 1.85 GHz that this load leaves, LDS free of bank
- * conflicts.  4096 tokens, 8 heads: dim 64 19 us, 128 27 us, 256 43 us; dims that
- * are not multiples of 16 pass through registers: 57 29 us, 200 97 us.  Short
- * sequences are bound by the two launches (about 9 us with the binding).
+ * Measured: 8192 causal tokens, 32 heads over 8, dim 128, bf16: 206 us, 1.33 PFLOP/s of the
+ * seen pairs (a large library product reaches 1.20 here); the matrix cores are busy 65 % of the
+ * cycles at the 1.85 GHz that this load leaves, LDS free of bank conflicts.  4096 tokens, 8 heads:
+ * dim 64 17 us, 128 23 us, 192 30 us, 256 37 us; dims that are not multiples of 16 pass through
+ * registers: 57 28 us.  Short sequences are bound by the two launches (about 9 us with
+ * the binding).
  */
 #include <hip/hip_runtime.h>
 
@@ -151,7 +151,6 @@ __global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a)
     constexpr int kStageBytes = kTileK * DP * 2;
     constexpr int kChunks = kStageBytes / 1024 / kQkWaves;   /* 1 KB loads of a wavefront per stage */
     __shared__ __attribute__((aligned(16))) char lds[2 * kStageBytes];
-    __shared__ float wmax[kQkWaves];
     const int tid = threadIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int per = a.heads / a.kv_heads;
@@ -176,6 +175,17 @@ __global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a)
     const int last_piece = a.dim / 8 - 1;
     const int frow = lane & 31, fhalf = lane >> 5;
     float best = -INFINITY;
+    /* one lane's pieces of a stage: byte offsets from its first key */
+    int voff[kChunks];
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        const int at = (wave * kChunks + c) * 64 + lane;
+        const int r = at / kPieces;
+        int p = (at % kPieces) ^ swizzle<DP>(r);
+        if constexpr (MODE == kSlices16)
+            p = p < last_piece ? p : last_piece;
+        voff[c] = (r * static_cast<int>(a.kst) + p * 8) * 2;
+    }
 
     for (int qt = tile0; static_cast<int64_t>(qt) * kTileQ < len_q; qt += a.q_tiles) {
         const int q0 = qt * kTileQ;
@@ -245,20 +255,13 @@ __global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a)
             const uint16_t* base = K + static_cast<int64_t>(k0) * a.kst;
             char* dst = lds + buf * kStageBytes;
             if constexpr (DIRECT) {
-                /* rows behind the end repeat the last one: in bounds, and masked */
+                /* rows behind the end are behind the descriptor's too: not read, and masked */
+                const int rows = left < kTileK ? left : kTileK;
                 const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
-                    const_cast<uint16_t*>(base), 0, 0x7fffffff, 0x00020000);
+                    const_cast<uint16_t*>(base), 0, ((rows - 1) * static_cast<int>(a.kst) + a.dim) * 2, 0x00020000);
 #pragma unroll
-                for (int c = 0; c < kChunks; ++c) {
-                    const int at = (wave * kChunks + c) * 64 + lane;
-                    const int r = at / kPieces;
-                    int p = (at % kPieces) ^ swizzle<DP>(r);
-                    if constexpr (MODE == kSlices16)
-                        p = p < last_piece ? p : last_piece;
-                    const int rr = r < left ? r : left - 1;
-                    buffer_load_lds16(rs, dst + (wave * kChunks + c) * 1024,
-                                      (rr * static_cast<int>(a.kst) + p * 8) * 2);
-                }
+                for (int c = 0; c < kChunks; ++c)
+                    buffer_load_lds16(rs, dst + (wave * kChunks + c) * 1024, voff[c]);
             } else {
                 /* two pieces at a time: all of them in flight spill beside the queries' registers */
 #pragma unroll 2
@@ -306,28 +309,51 @@ __global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a)
                         for (int r = 0; r < 16; ++r)
                             best = maximum(best, acc[i][j][r]);
             } else {
-                /* acc[i][j][r]: key k0 + 32 i + 8 (r / 4) + 4 (lane / 32) + r % 4, query of this lane */
+                /* acc[i][j][r]: key k0 + 4 (lane / 32) + 32 i + 8 (r / 4) + r % 4, query of this lane;
+                 * a tile at one of the two edges is compared with that one's limit only */
+                auto masked = [&](auto lo_side, auto hi_side) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
+                    for (int j = 0; j < 2; ++j) {
+                        const int l = klo[j] - k0 - 4 * fhalf, u = khi[j] - k0 - 4 * fhalf;
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int r = 0; r < 16; ++r) {
-                            const int key = k0 + 32 * i + 8 * (r >> 2) + 4 * fhalf + (r & 3);
-                            best = maximum(best, key >= klo[j] && key <= khi[j] ? acc[i][j][r] : -INFINITY);
-                        }
+                            for (int r = 0; r < 16; ++r) {
+                                const int key = 32 * i + 8 * (r >> 2) + (r & 3);
+                                const bool seen = (!lo_side.value || key >= l) && (!hi_side.value || key <= u);
+                                best = maximum(best, seen ? acc[i][j][r] : -INFINITY);
+                            }
+                    }
+                };
+                if (k0 >= every_lo)
+                    masked(std::false_type{}, std::true_type{});
+                else if (k0 + kTileK - 1 <= every_hi)
+                    masked(std::true_type{}, std::false_type{});
+                else
+                    masked(std::true_type{}, std::true_type{});
             }
         };
 
-        /* one barrier per stage: behind it every wavefront's part of stage kt is in LDS, and the
-         * other buffer is no longer read */
         __syncthreads();   /* the buffers of the previous query tile */
         stage(t0, 0);
         for (int kt = t0; kt < t1; ++kt) {
             const int buf = (kt - t0) & 1;
-            __syncthreads();
+            /* Behind the barrier every wavefront's part of stage kt is in LDS, and the other buffer is
+             * no longer read.  The wait for this wavefront's own loads and LDS accesses is written
+             * out: nothing else makes the loads into LDS land before it.  (Three and four buffers with
+             * loads further ahead are no faster: 4096 tokens, dim 128, 23.0 and 23.6 us, two 22.4.) */
+            if constexpr (DIRECT) {
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_waitcnt(0x0070);   /* gfx9 encoding: vmcnt(0) lgkmcnt(0) */
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+            } else {
+                __syncthreads();
+            }
             if (kt + 1 < t1)
                 stage(kt + 1, buf ^ 1);
+            if constexpr (DIRECT)
+                __builtin_amdgcn_sched_barrier(0);
             compute(kt, buf);
         }
     }
@@ -335,6 +361,11 @@ __global__ __launch_bounds__(kQkThreads, 2) void k_qk_max(QkArgs a)
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1)
         best = maximum(best, __shfl_xor(best, d, 64));
+    /* In the stages' array: beside a second LDS variable the compiler waits for all loads in flight
+     * before a stage's first fragment read, and nothing overlaps (4096 tokens, dim 128: 26.7 us, so
+     * 22.4). */
+    float* wmax = reinterpret_cast<float*>(lds);
+    __syncthreads();
     if (lane == 0)
         wmax[wave] = best;
     __syncthreads();
