@@ -1348,15 +1348,19 @@ hipError_t ns_step(const TensorDesc* d_desc, const MuonInfo* d_info, const MuonB
  * Bound by the matrix cores at the clock they leave themselves; measured on 4096 x 14336
  * (4.33 ms in all): norm 57 us and input 95 us (HBM), Gram 247 us in three parts of its depth +
  * 33 us for their sum, A A^T 97 us, step 505 us (its epilogue moves 10 bytes per element), last
- * step 457 us.  3 x 1000 x 333: 17 launches of 6 to 9 us, 139 us. */
+ * step 457 us.  3 x 1000 x 333: 17 launches of 6 to 9 us, 133 us. */
 constexpr int kSumThreads = 512;
 constexpr int64_t kSumMax = 512;      /* partial sums of squares per matrix, at most */
-constexpr int64_t kSumPer = 8192;     /* elements a workgroup sums at the least */
+constexpr int64_t kSumRun = 1024;     /* columns of one row that a wavefront takes at a time */
 
-int64_t sum_parts(int64_t rows, int64_t cols)
+/* Workgroups per matrix: a run for each wavefront until the chip's 8192 resident wavefronts are
+ * filled, then longer ones (3 x 1000 x 333 takes 133 us in all so, 139 with 8192 elements a
+ * workgroup; large stacks the same either way). */
+int64_t sum_parts(int64_t batch, int64_t rows, int64_t cols)
 {
-    const int64_t p = (rows * cols + kSumPer - 1) / kSumPer;
-    return p < 1 ? 1 : (p > kSumMax ? kSumMax : p);
+    const int64_t runs = rows * ((cols + kSumRun - 1) / kSumRun);
+    const int64_t per = kSumThreads / 64 * ((batch * runs + 8191) / 8192);
+    return std::min((runs + per - 1) / per, kSumMax);
 }
 
 /* Momentum update in place and the partial sums of g~^2 (grid: parts, batch). */
@@ -1368,11 +1372,11 @@ __global__ __launch_bounds__(kSumThreads) void k_stack_momentum(OrthoSrc s, doub
     const GradVals v = grad_vals(s.sc);
     const int64_t z = blockIdx.y;
     double acc = 0.0;
-    /* a wavefront takes a run of 1024 columns of one row, four elements a lane and access */
+    /* a wavefront takes a run of columns of one row, four elements a lane and access */
     const int64_t wave = static_cast<int64_t>(blockIdx.x) * (kSumThreads / 64) + (threadIdx.x >> 6);
     const int64_t waves = static_cast<int64_t>(gridDim.x) * (kSumThreads / 64);
     const int lane = threadIdx.x & 63;
-    constexpr int64_t kRun = 1024;
+    constexpr int64_t kRun = kSumRun;
     const int64_t runs = (s.cols + kRun - 1) / kRun;
     for (int64_t t = wave; t < s.rows * runs; t += waves) {
         const int64_t i = t / runs, c0 = (t % runs) * kRun + 4 * lane;
@@ -1604,7 +1608,7 @@ OrthoPlan ortho_plan(int64_t batch, int64_t rows, int64_t cols)
     p.tile = pick_tile(batch, p.m, p.n);
     p.mp = pad_to(p.m, p.tile);
     p.np = pad_to(p.n, p.tile);
-    p.parts = sum_parts(rows, cols);
+    p.parts = sum_parts(batch, rows, cols);
     p.kparts = pick_parts(batch, p.m, p.n, p.tile);
     const int64_t mt = p.mp / p.tile;
     p.slot = 2 * (4 * p.mp * p.np + 2 * p.mp * p.mp);

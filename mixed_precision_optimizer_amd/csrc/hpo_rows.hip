@@ -12,7 +12,7 @@
  * Measured: 4096 x 14336, bf16 O and weight: statistics 24 us (4.9 TB/s of O), update 108 us
  * (6.5 TB/s of its 12 bytes per element); 16 x 1024 x 2048 with 8-bit weights 16 and 58 us; 129 x 257:
  * 4 and 4 us, 11 us with the binding.  Clip of one layer (4096 x 4096 and 1024 x 4096
- * rows, nearly all clipped): 37 us, 5.7 TB/s.
+ * rows, nearly all clipped): 37 to 40 us, 5.3 to 5.7 TB/s.
  *
  * Floating point: built with -ffp-contract=off; every elementwise operation
  * rounds on its own, in the order written.

@@ -1,7 +1,7 @@
 /*
  * hpo_stack_impl.h -- layouts shared by the stack operators' host code
  * (hpo_stack_api.cpp) and their kernels (hpo_rows.hip, hpo_qk.hip,
- * hpo_muon.hip).  Not part of the public ABI.
+ * hpo_gram.hip, hpo_muon.hip).  Not part of the public ABI.
  */
 #ifndef HPO_STACK_IMPL_H
 #define HPO_STACK_IMPL_H
@@ -27,7 +27,6 @@ struct WeightView {
     uint8_t* scales;    /* HPO_WEIGHT_MX8 */
     int64_t rows, cols;
     int32_t param_dtype;   /* HPO_PARAM_FP32 (none), HPO_PARAM_BF16 or HPO_WEIGHT_MX8 */
-    int32_t reserved;
 };
 
 struct RmsArgs {
@@ -63,7 +62,6 @@ struct ClipArgs {
     double tau;
     int32_t heads, kv_heads;
     int32_t n;
-    int32_t reserved;
     ClipItem item[HPO_CLIP_MAX_WEIGHTS];
 };
 
