@@ -16,8 +16,8 @@
  * each lane keeps one number, folded with v_maximum3 (two logits an
  * instruction, NaN stays NaN).
  *
- * Measured: 8192 causal tokens, 32 heads over 8, dim 128, bf16: 206 us, 1.33 PFLOP/s of the
- * seen pairs (a large library product reaches 1.20 here); the matrix cores are busy 65 % of the
+ * Measured: 8192 causal tokens, 32 heads over 8, dim 128, bf16: 206 to 216 us from box to box, 1.27
+ * to 1.33 PFLOP/s of the seen pairs (a large library product reaches 1.20 here); the matrix cores are busy 65 % of the
  * cycles at the 1.85 GHz that this load leaves, LDS free of bank conflicts.  4096 tokens, 8 heads:
  * dim 64 17 us, 128 23 us, 192 30 us, 256 37 us; dims that are not multiples of 16 pass through
  * registers: 57 28 us.  Short sequences are bound by the two launches (about 9 us with
