@@ -440,8 +440,11 @@ hipError_t launch_qk_max(QkArgs a, bool fp16, bool aligned, hipStream_t stream)
     a.q_tiles = (a.max_q + kTileQ - 1) / kTileQ;
     const int64_t tiles = static_cast<int64_t>(a.batch) * a.heads * a.q_tiles;
     /* Few query tiles: the keys are split until the chip's 512 resident workgroups have work, with
-     * four stages each at the least. */
-    const int64_t want = (512 + tiles - 1) / tiles, most = (a.max_k + 4 * kTileK - 1) / (4 * kTileK);
+     * four stages each at the least.  Up to 64 queries keep one wavefront of a workgroup busy, and dims
+     * up to 128 leave room for a third one: 768 (4 x 1 query on 9000 keys, 32 heads over 8: 38 us, with
+     * 512 52, with 1024 55; longer queries lose 3 to 12 % with it). */
+    const int64_t wgs = a.max_q <= kWaveRows && a.dim <= 128 ? 768 : 512;
+    const int64_t want = (wgs + tiles - 1) / tiles, most = (a.max_k + 4 * kTileK - 1) / (4 * kTileK);
     a.splits = static_cast<int32_t>(want < most ? want : most);
     if (a.splits < 1)
         a.splits = 1;
