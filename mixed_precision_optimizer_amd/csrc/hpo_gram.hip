@@ -36,6 +36,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "hpo_muon_device.h"
 
@@ -51,6 +52,7 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256;
 constexpr int kTileElems = 8192;   /* elements of a column tile: 32 per thread */
 constexpr int kTop = 14;           /* values are scaled to at most 2^14 */
+constexpr double kSmallShare = 0x1p-10;   /* of ||g~|| in ||g~|| + eps, below which X0 is scaled up */
 
 struct GramArgs {
     OrthoSrc s;
@@ -61,7 +63,7 @@ struct GramArgs {
     float* part;         /* [batch][chunks][MP][MP] */
     int32_t* part_exp;   /* [batch][chunks] */
     uint16_t* P;         /* [batch][2][MP][MP]: h and l of P * 2^p_exp */
-    float* inv;          /* [batch][2]: 2^-14 d as (mantissa of 1 / d, exponent) */
+    float* inv;          /* [batch][3]: 1 / d as (mantissa, exponent of X0's scale), and the result's exponent */
     uint16_t* out;
     int64_t obs, ors;
     int32_t steps;
@@ -567,18 +569,26 @@ __device__ __forceinline__ void iterate(const GramArgs& a, int64_t z, int wave, 
         trace += __shfl_xor(trace, off, 64);
     __syncthreads();
     /* d = ||g~|| + eps; the sums are at scale 2^(2 (kTop - top)) */
-    const double unit = ldexp(1.0, top > -1000 ? top - kTop : 0);
-    const float d = static_cast<float>(sqrt(trace) * unit) + a.s.sc.eps;
-    const double id = d == 0.0f ? 0.0 : 1.0 / static_cast<double>(d);
+    const double unit = ldexp(1.0, top > -1000 ? top - kTop : 0), norm = sqrt(trace) * unit;
+    const float df = static_cast<float>(norm) + a.s.sc.eps;
+    /* under fp32's normal numbers the sum stays in binary64: a subnormal keeps few bits, or none */
+    const double d = df < FLT_MIN ? norm + static_cast<double>(a.s.sc.eps) : static_cast<double>(df);
+    const double id = d == 0.0 ? 0.0 : 1.0 / d;
+    /* A norm far under eps leaves X0 far under 1, and its two fp16 values would keep few bits: X0 and
+     * the result are held 2^lift larger (P does not depend on X0's scale). */
+    const double share = norm * id;
+    const int lift = share > 0.0 && share < kSmallShare ? -1 - ilogb(share) : 0;
     /* the factor of A as a value in [1/2, 1) and an exponent */
     int fe = 0;
     const float fm = static_cast<float>(frexp(trace == 0.0 ? 0.0 : (unit * id) * (unit * id), &fe));
     if (tid == 0) {
-        /* 1 / d as mantissa and exponent: it may lie beyond fp32's range */
+        /* 1 / d as mantissa and exponent: it may lie beyond fp32's range.  0 (d beyond it) takes no
+         * scale, which would make an infinity of large elements. */
         int e = 0;
         const double mant = frexp(id, &e);
-        a.inv[2 * z] = static_cast<float>(mant);
-        a.inv[2 * z + 1] = static_cast<float>(e + kTop);
+        a.inv[3 * z] = static_cast<float>(mant);
+        a.inv[3 * z + 1] = id == 0.0 ? 0.0f : static_cast<float>(e + kTop + lift);
+        a.inv[3 * z + 2] = static_cast<float>(-(a.p_exp + kTop + lift));
     }
 #pragma unroll
     for (int j = 0; j < BN; ++j)
@@ -732,8 +742,8 @@ __device__ __forceinline__ void apply(const GramArgs& a, int64_t z, int64_t chun
     const GradVals gv = grad_vals(a.s.sc);
     const int64_t c0 = chunk * a.run;
     const int64_t c1 = c0 + a.run < a.n ? c0 + a.run : a.n;
-    const float mant = a.inv[2 * z];
-    const int ex = static_cast<int>(a.inv[2 * z + 1]);
+    const float mant = a.inv[3 * z];
+    const int ex = static_cast<int>(a.inv[3 * z + 1]), down = static_cast<int>(a.inv[3 * z + 2]);
     const int i0 = (wave % kRowBlocks) * 32, j0 = (wave / kRowBlocks) * 64;
     u32x4_t ph[kSlices], pl[kSlices];
     const uint16_t* P = a.P + z * (2 * MP * MP);
@@ -756,7 +766,7 @@ __device__ __forceinline__ void apply(const GramArgs& a, int64_t z, int64_t chun
             float y[8];
 #pragma unroll
             for (int t = 0; t < 8; ++t)
-                y[t] = __builtin_ldexpf(Sh::at(v, q, t) * mant, ex);
+                y[t] = __builtin_ldexpf(Sh::at(v, q, t), ex) * mant;   /* scaled first: it may be subnormal */
             u32x4_t h, l;
             split8<1>(y, h, l);
             int r, c;
@@ -786,7 +796,6 @@ __device__ __forceinline__ void apply(const GramArgs& a, int64_t z, int64_t chun
                 }
             }
         }
-        const int down = -(a.p_exp + kTop);
         char* out = reinterpret_cast<char*>(a.out + z * a.obs);
         const uint32_t ors = static_cast<uint32_t>(a.ors);
 #pragma unroll
@@ -861,7 +870,7 @@ GramPlan gram_plan(int64_t batch, int64_t rows, int64_t cols)
     per = (tiles + p.chunks - 1) / p.chunks;
     p.chunks = (tiles + per - 1) / per;
     p.run = per * kc;
-    p.slot = (4 * p.chunks + 4) * p.mp * p.mp + 4 * p.chunks + 8;
+    p.slot = (4 * p.chunks + 4) * p.mp * p.mp + 4 * p.chunks + 12;
     constexpr int64_t kCap = int64_t{4} << 30;
     const int64_t most = kCap / p.slot > 1 ? kCap / p.slot : 1;
     const int64_t slices = (batch + most - 1) / most;
@@ -935,7 +944,7 @@ hipError_t launch_gram(const OrthoArgs& o, hipStream_t stream)
         a.P = reinterpret_cast<uint16_t*>(at);
         at += 4 * p.count * p.mp * p.mp;
         a.inv = reinterpret_cast<float*>(at);
-        at += 8 * p.count;
+        at += 12 * p.count;
         a.part_exp = reinterpret_cast<int32_t*>(at);
         a.out = static_cast<uint16_t*>(o.out.data) + z0 * o.out.bs;
         a.obs = o.out.bs;

@@ -6,7 +6,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import stack_util as su  # noqa: E402
-from test_gpu_stack import CFG, DEV, S, check_rms, gen, workspace  # noqa: E402, F401
+from test_gpu_stack import CFG, DEV, S, check_ortho, check_rms, gen, gradient, ortho, workspace  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +66,59 @@ def test_rms_update_factors_beyond_fp32_leave_rows_of_zeros(S):
         S.hpo_rms_update(O.to(DEV), W, v, S.make_rms_cfg(**cfg), workspace(S.hpo_rms_update_workspace(W)))
         keep = W0 * torch.tensor(1 - cfg["lr"] * cfg["weight_decay"], dtype=torch.float32)
         assert torch.equal(W[0, 1:].cpu(), keep[0, 1:]), cfg
+
+
+# --------------------------------------------------------------------------
+# hpo_orthogonalize: norms far under ns_eps, or under fp32's normal numbers
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("r,c", [(40, 60), (60, 40), (90, 3000), (20000, 128)])
+@pytest.mark.parametrize("below", [1e-2, 1e-4, 1e-8, 1e-12, 1e-20, 1e-28])
+def test_orthogonalize_gradients_far_below_eps(S, r, c, below):
+    """The iteration is all but linear there; its direction and size are as exact as anywhere else."""
+    G = gradient(111, 2, r, c).double()
+    G = (G / torch.linalg.vector_norm(G, dim=(1, 2), keepdim=True) * 1e-7 * below).float()
+    G[1] *= 1e6 / below * 1e-3      # one matrix at an ordinary norm beside it
+    check_ortho(ortho(S, G.to(DEV)), G.double(), tag=f"norm {below} eps")
+
+
+@pytest.mark.parametrize("r,c", [(40, 60), (300, 20), (90, 3000)])
+@pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-7])
+@pytest.mark.parametrize("momentum", [False, True])
+def test_orthogonalize_subnormal_gradients(S, r, c, eps, momentum):
+    """Gradients of a few of fp32's least steps: dense, and two elements of one row."""
+    step = 2.0 ** -149
+    G = torch.zeros(2, r, c)
+    G[0] = torch.randint(-3, 4, (r, c), generator=gen(113)).float() * step
+    G[1, r // 2, 3], G[1, r // 2, c - 1] = step, step
+    cfg = S.hpo.make_muon_cfg(ns_eps=eps, momentum=0.5, nesterov=False)
+    M = 4.0 * G if momentum else None      # 0.5 * 4 G + G: exact
+    m = M.to(DEV) if momentum else None
+    out = ortho(S, G.to(DEV), m, cfg=cfg)
+    g = 3.0 * G if momentum else G
+    if momentum:
+        assert torch.equal(m.cpu(), g)
+    # the library holds eps as fp32
+    check_ortho(out, g.double(), eps=float(torch.tensor(eps, dtype=torch.float32)), tag=f"subnormal, eps {eps}")
+
+
+def test_orthogonalize_beyond_fp32_still_gives_zeros(S):
+    """A norm over fp32's largest value gives zeros."""
+    for r, c in ((40, 60), (100, 3000), (140, 150)):
+        assert bool((ortho(S, torch.full((1, r, c), 3e38, device=DEV)) == 0).all())
+
+
+@pytest.mark.parametrize("r,c", [(40, 300), (100, 3000)])
+def test_orthogonalize_far_below_eps_in_a_graph(S, r, c):
+    """The exponent that such a matrix is held at belongs to each run of the graph."""
+    G = gradient(115, 2, r, c).to(DEV)
+    out, ws = torch.zeros(G.shape, dtype=torch.bfloat16, device=DEV), workspace(S.hpo_orthogonalize_workspace(G))
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        ortho(S, G, out=out, ws=ws)
+    for size in (1.0, 1e-20, 1e-9, 1.0, 1e-25):
+        G.copy_(gradient(117, 2, r, c) * size)
+        gr.replay()
+        got = su.bits(out)
+        torch.cuda.synchronize()
+        assert torch.equal(got, su.bits(ortho(S, G))), size
+        check_ortho(out, G.double().cpu(), tag=f"graph, size {size}")
