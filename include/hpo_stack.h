@@ -115,9 +115,9 @@ hpo_status hpo_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols
  * bf16, or to HPO_WEIGHT_MX8 with d_scales.  beta2 = 0 is the plain
  * root-mean-square norm of each row (d_v may then be NULL; it is written, not
  * read, if it is given).  Squares and the mean are summed in fp32 per lane and in
- * binary64 across lanes; N, s and r in binary64 (r at most 2^500, s r_i at most fp32's
- * largest value in magnitude: rows of zeros stay).  The sums' order is fixed: the
- * same inputs give the same bits.
+ * binary64 across lanes; N and s in binary64, r_i rounded to fp32 where it meets s (r_i
+ * and s r_i at most fp32's largest value in magnitude: rows of zeros stay).  The sums'
+ * order is fixed: the same inputs give the same bits.
  * 0 <= beta2 < 1; eps >= 0, and a row with sqrt(v_i) + eps = 0 is left out of the
  * update; lr, weight_decay and target_rms are finite.  A stack has at most 2^24 rows
  * in all.  O, the master, the model weight, d_scales and d_v do not overlap.

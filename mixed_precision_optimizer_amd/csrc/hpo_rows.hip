@@ -20,6 +20,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 
 #include "hpo_device.h"
 #include "hpo_stack_impl.h"
@@ -210,11 +211,10 @@ __device__ __forceinline__ bool skipped(const int32_t* d_found) { return d_found
 /* hpo_rms_update                                                          */
 /* ---------------------------------------------------------------------- */
 constexpr int kStatRows = 4;    /* rows of a workgroup, one wavefront each */
-constexpr double kLeastDen = 0x1p-500;   /* keeps r, its square and N^2 inside binary64 */
-constexpr double kMost32 = 3.4028234663852886e38, kMost64 = 1.7976931348623157e308;
 
-/* x, or the nearest end of [-most, most]; NaN stays NaN. */
-__device__ __forceinline__ double within(double x, double most) { return x > most ? most : (x < -most ? -most : x); }
+/* x, the largest finite value in place of an infinity. */
+__device__ __forceinline__ float finite(float x) { return __builtin_isinf(x) ? __builtin_copysignf(FLT_MAX, x) : x; }
+__device__ __forceinline__ double finite(double x) { return __builtin_isinf(x) ? __builtin_copysign(DBL_MAX, x) : x; }
 
 /* Squares of eight consecutive elements, n of them in the row. */
 template <typename OT>
@@ -243,10 +243,10 @@ __device__ __forceinline__ double finish_row(const RmsArgs& a, int64_t idx, doub
         a.v[idx] = v;
     }
     const double den = sqrt(static_cast<double>(v)) + a.eps;
-    /* Only a row with v = 0 comes to the limit, and every such row comes to the same 1 / eps: its ratio
-     * to the rows with v > 0 (at most 2^75) is beyond binary64's bits either way. */
-    const double r = den == 0.0 ? 0.0 : (den < kLeastDen ? 1.0 / kLeastDen : 1.0 / den);
-    a.r[idx] = r;
+    /* Finite in fp32: only a row with v = 0 comes to the limit, and every such row comes to the same
+     * 1 / eps; its ratio to the rows with v > 0 (at most 2^75) is beyond binary64's bits either way. */
+    const double r = den == 0.0 ? 0.0 : (den * FLT_MAX < 1.0 ? FLT_MAX : 1.0 / den);
+    a.r[idx] = static_cast<float>(r);
     return tot * r * r;
 }
 
@@ -369,13 +369,13 @@ __global__ __launch_bounds__(kRowThreads) void k_rms_apply(RmsArgs a)
         n2 = total;
     }
     /* finite, as the coefficients are: a row of zeros, or one with r = 0, stays where it is */
-    const double s = n2 > 0.0 ? within(a.gain / sqrt(n2), kMost64) : 0.0;
+    const double s = n2 > 0.0 ? finite(a.gain / sqrt(n2)) : 0.0;
     each_piece<U>(rows, cols, blockIdx.x, a.rounds, [&](const Spot(&p)[U], int n) {
         f32x4_t o[U], x[U];
         float c[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            c[u] = static_cast<float>(within(s * a.r[z * rows + p[u].row], kMost32));
+            c[u] = finite(static_cast<float>(s * static_cast<double>(a.r[z * rows + p[u].row])));
             o[u] = load4(static_cast<const OT*>(a.O.data) + z * a.O.bs + p[u].row * a.O.rs + p[u].col, p[u].n);
             x[u] = load4<NT>(static_cast<const float*>(a.w.master.data) + z * a.w.master.bs + p[u].row * a.w.master.rs +
                                  p[u].col,

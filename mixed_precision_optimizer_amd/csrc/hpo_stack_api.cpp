@@ -362,8 +362,8 @@ hpo_status hpo_rms_update_workspace(int64_t batch, int64_t rows, int64_t* out_by
         return fail(HPO_EINVAL, "out_bytes is NULL");
     if (batch < 0 || rows < 0 || batch > kMaxBatch || rows > HPO_MUON_MAX_DIM || batch * rows > kMaxRows)
         return fail(HPO_EINVAL, "bad shape: %lld matrices of %lld rows", (long long)batch, (long long)rows);
-    /* q, N^2 and r in binary64 */
-    *out_bytes = batch * rows == 0 ? 0 : 8 * batch * rows + 8 * batch + 8 * batch * rows;
+    /* q and N^2 in binary64, r in fp32 */
+    *out_bytes = batch * rows == 0 ? 0 : 8 * batch * rows + 8 * batch + 4 * batch * rows;
     return ok();
 }
 
@@ -411,7 +411,7 @@ hpo_status hpo_rms_update(const hpo_stack* O, const hpo_stack* master, float* d_
     const int64_t n = master->batch * master->rows;
     a.q = static_cast<double*>(d_workspace);
     a.norm2 = a.q + n;
-    a.r = a.norm2 + master->batch;
+    a.r = reinterpret_cast<float*>(a.norm2 + master->batch);
     a.beta2 = cfg->beta2;
     a.eps = cfg->eps;
     a.gain = cfg->lr * cfg->target_rms * std::sqrt(static_cast<double>(master->rows) * static_cast<double>(master->cols));

@@ -34,7 +34,7 @@ struct RmsArgs {
     WeightView w;
     float* v;        /* [batch][rows], nullable */
     double* q;       /* [batch][parts] sums of cols * ms * r^2 over a part's rows */
-    double* r;       /* [batch][rows] 1 / (sqrt(v) + eps) */
+    float* r;        /* [batch][rows] 1 / (sqrt(v) + eps) */
     double* norm2;   /* [batch], written by the fold (large stacks only) */
     int64_t batch;
     int64_t parts;
