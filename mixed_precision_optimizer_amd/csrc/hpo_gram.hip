@@ -52,7 +52,6 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 constexpr int kThreads = 256;
 constexpr int kTileElems = 8192;   /* elements of a column tile: 32 per thread */
 constexpr int kTop = 14;           /* values are scaled to at most 2^14 */
-constexpr double kSmallShare = 0x1p-10;   /* of ||g~|| in ||g~|| + eps, below which X0 is scaled up */
 
 struct GramArgs {
     OrthoSrc s;
@@ -576,8 +575,8 @@ __device__ __forceinline__ void iterate(const GramArgs& a, int64_t z, int wave, 
     const double id = d == 0.0 ? 0.0 : 1.0 / d;
     /* A norm far under eps leaves X0 far under 1, and its two fp16 values would keep few bits: X0 and
      * the result are held 2^lift larger (P does not depend on X0's scale). */
-    const double share = norm * id;
-    const int lift = share > 0.0 && share < kSmallShare ? -1 - ilogb(share) : 0;
+    const int lift =
+        norm > 0.0 && norm < kSmallShare * static_cast<double>(a.s.sc.eps) ? -1 - ilogb(norm * id) : 0;
     /* the factor of A as a value in [1/2, 1) and an exponent */
     int fe = 0;
     const float fm = static_cast<float>(frexp(trace == 0.0 ? 0.0 : (unit * id) * (unit * id), &fe));

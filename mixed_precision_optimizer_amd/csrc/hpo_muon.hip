@@ -58,6 +58,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -382,6 +383,7 @@ struct GemmArgs {
     uint16_t* XL;        /* f16 step: what the rounding of X lost, as lo_at() lays it out */
     int64_t sxl;
     int32_t lo_out;      /* f16 step: the next step wants it (written in place) */
+    const int32_t* lift; /* f16 gram / sum / out: X of matrix z is held 2^lift[z] larger */
     uint16_t* out16;     /* f16 out: bf16 result */
     int64_t oss, ors;    /* its matrix and row strides */
     float* part;         /* f16 part / sum: [matrix][part of k][tile][register order] */
@@ -500,6 +502,9 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
         return;
     __shared__ __attribute__((aligned(16))) char lds[T::kLdsBytes];
     const int64_t z = blockIdx.z;
+    int lift = 0;
+    if constexpr (EPI == kEpiF16Gram || EPI == kEpiF16Sum || EPI == kEpiF16Out)
+        lift = g.lift[z];
     int64_t ty, tx;
     tile_of<SYM>(g, ty, tx);
     const int64_t row0 = ty * kBM;
@@ -941,6 +946,7 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
         if constexpr (EPI == kEpiGram || EPI == kEpiPoly || EPI == kEpiF16Gram || EPI == kEpiF16Poly ||
                       EPI == kEpiF16Sum) {
             constexpr bool kPoly = EPI == kEpiPoly || EPI == kEpiF16Poly;
+            const float gc = __builtin_ldexpf(g.c, -2 * lift);
             const bool diag = SYM && ty == tx;
             if constexpr (kPoly) {
                 /* A is symmetric and stored whole: column j of the tile is row col0 + j */
@@ -962,7 +968,7 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
                         if constexpr (EPI == kEpiF16Gram || EPI == kEpiF16Sum) {
 #pragma clang loop unroll(full)
                             for (int e = 0; e < 4; ++e)
-                                x[e] = g.c * x[e];
+                                x[e] = gc * x[e];
                         }
                         if constexpr (kPoly) {
                             const u32x2_t av = *pt;
@@ -1075,7 +1081,7 @@ __global__ __launch_bounds__(T::kThreads, T::kWavesPerSimd) void k_ns_gemm(GemmA
 #pragma clang loop unroll(full)
                         for (int e = 0; e < 4; ++e) {
                             const float ax = g.a * unpack(xv, e), cx = g.c * acc[ti][tj][4 * q + e];
-                            b[e] = bf16_rne_bits(ax + cx);
+                            b[e] = bf16_rne_bits(__builtin_ldexpf(ax + cx, -lift));
                         }
                         u32x2_t t;
                         t.x = b[0] | (b[1] << 16);
@@ -1436,18 +1442,23 @@ __device__ __forceinline__ int64_t lo_at(int32_t tile, int64_t i, int64_t j, int
 
 /* X0 = f16(g~ / (norm + eps) * 2^ex) both ways round, zero-padded, and what the
  * rounding lost (grid: padded columns / 64, rows / 64, batch; natural
- * orientation, as k_muon_ns_input). */
+ * orientation, as k_muon_ns_input).
+ * A norm far under eps leaves X0 far under 1, where fp16 keeps few bits. The iteration is linear
+ * there, so such a matrix is held 2^lift larger (lift is written for the products that are
+ * not): X and the terms of a X + B X scale with it, A = X X^T takes 2^(-2 lift), the
+ * result 2^-lift.  `room` = log2 of what X may grow by over the bounds that its scales were made for. */
 template <bool BF16>
 __global__ __launch_bounds__(kBlock) void k_stack_input(OrthoSrc s, const double* part, int32_t parts, float x0_scale,
                                                         uint16_t* copy, int64_t ld_copy, uint16_t* trans,
                                                         int64_t ld_trans, int64_t stride, uint16_t* lo,
-                                                        int32_t lo_tile, int32_t tall)
+                                                        int32_t lo_tile, int32_t tall, int32_t room, int32_t* lift_out)
 {
     if (!gate_open(s.sc.gate))
         return;
     __shared__ __attribute__((aligned(4))) uint16_t tile[kTile][kTile + 2];
     __shared__ __attribute__((aligned(4))) uint16_t tlo[kTile][kTile + 2];
     __shared__ float dnorm;
+    __shared__ int32_t up, lift;   /* g~ 2^up / dnorm = X0 2^lift */
     const GradVals k = grad_vals(s.sc);
     const int64_t z = blockIdx.z;
     const int64_t r0 = static_cast<int64_t>(blockIdx.y) * kTile;
@@ -1457,10 +1468,25 @@ __global__ __launch_bounds__(kBlock) void k_stack_input(OrthoSrc s, const double
     for (int32_t p = tid; p < parts; p += kBlock)
         acc += part[z * parts + p];
     const double tot = block_sum<kBlock>(acc);
-    if (tid == 0)
-        dnorm = static_cast<float>(sqrt(tot)) + s.sc.eps;
+    if (tid == 0) {
+        const double norm = sqrt(tot), d64 = norm + static_cast<double>(s.sc.eps);
+        lift = 0;
+        if (norm > 0.0 && norm < kSmallShare * static_cast<double>(s.sc.eps)) {
+            const int32_t free = -1 - ilogb(norm / d64) - room;
+            lift = free > 0 ? free : 0;
+        }
+        up = lift;
+        dnorm = static_cast<float>(norm) + s.sc.eps;
+        if (dnorm < FLT_MIN) {   /* a subnormal keeps few bits, or none */
+            dnorm = static_cast<float>(ldexp(d64, 64));
+            up += 64;
+        }
+        if (blockIdx.x == 0 && blockIdx.y == 0)
+            lift_out[z] = lift;
+    }
     __syncthreads();
     const float d = dnorm;
+    const int to = up;
     constexpr int kPer = kTile * kTile / 4 / kBlock;
     f32x4_t x[kPer], mom[kPer];
 #pragma unroll
@@ -1485,7 +1511,7 @@ __global__ __launch_bounds__(kBlock) void k_stack_input(OrthoSrc s, const double
             if (s.M != nullptr)
                 g = nesterov_of(g, mom[q][t], s.sc);
             /* 0 / 0 is a matrix of zeros with eps = 0: it stays 0, as does what lies behind the edge */
-            const float y = g == 0.0f || t >= left ? 0.0f : g / d * x0_scale;
+            const float y = g == 0.0f || t >= left ? 0.0f : __builtin_ldexpf(g, to) / d * x0_scale;
             const uint32_t h = f16_bits(y);
             tile[r][c + t] = static_cast<uint16_t>(h);
             tlo[r][c + t] = static_cast<uint16_t>(f16_bits((y - f16v(static_cast<uint16_t>(h))) * kLoScale));
@@ -1534,6 +1560,7 @@ __global__ __launch_bounds__(kBlock) void k_stack_input(OrthoSrc s, const double
 /* Buffers of one slice of a stack. */
 struct OrthoWork {
     double* part;
+    int32_t* lift;
     uint16_t *X, *XT[2], *XL, *A, *B;
 };
 
@@ -1632,6 +1659,8 @@ hipError_t ortho_slice(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64
     char* at = static_cast<char*>(a.ws);
     w.part = reinterpret_cast<double*>(at);
     at += round256(8 * p.count * p.parts);
+    w.lift = reinterpret_cast<int32_t*>(at);
+    at += round256(4 * p.count);
     const int64_t xs = p.mp * p.np, as = p.mp * p.mp;
     auto take = [&](int64_t elems) {
         uint16_t* r = reinterpret_cast<uint16_t*>(at);
@@ -1658,7 +1687,7 @@ hipError_t ortho_slice(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64
                 dim3(static_cast<uint32_t>(Cp / kTile), static_cast<uint32_t>(Rp / kTile), cnt), kBlock, stream, s,
                 static_cast<const double*>(w.part), static_cast<int32_t>(p.parts), a.x0_scale, tall ? w.XT[0] : w.X,
                 tall ? p.mp : p.np, tall ? w.X : w.XT[0], tall ? p.np : p.mp, xs, lo0 ? w.XL : nullptr, p.tile,
-                static_cast<int32_t>(tall ? 1 : 0));
+                static_cast<int32_t>(tall ? 1 : 0), a.lift_room, w.lift);
     if (e != hipSuccess)
         return e;
     const MuonUpdate up{};
@@ -1668,6 +1697,7 @@ hipError_t ortho_slice(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64
         const NsStepScale& f = a.step[k];
         GemmArgs g{};
         g.gate = a.sc.gate;
+        g.lift = w.lift;
         g.P = w.X; g.ldp = p.np; g.sp = xs;
         g.Q = w.X; g.ldq = p.np; g.sq = xs;
         g.K = static_cast<int32_t>(p.np);
@@ -1754,7 +1784,7 @@ hipError_t ortho_tiles(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64
 int64_t ortho_workspace(int64_t batch, int64_t rows, int64_t cols)
 {
     const OrthoPlan p = ortho_plan(batch, rows, cols);
-    return round256(8 * p.count * p.parts) + p.count * p.slot;
+    return round256(8 * p.count * p.parts) + round256(4 * p.count) + p.count * p.slot;
 }
 
 hipError_t launch_orthogonalize(const OrthoArgs& a, hipStream_t stream)

@@ -114,6 +114,10 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef f32x4_t f32x4_any __attribute__((aligned(4)));
 typedef u32x2_t u32x2_any __attribute__((aligned(2)));
 
+/* ||g~|| / eps below which X0 is held larger than it is: the iteration's cubic terms are
+ * under 2^-18 of its linear ones there. */
+constexpr double kSmallShare = 0x1p-10;
+
 /* Four consecutive stored elements: n of them are there (the others read as 0). */
 template <bool BF16>
 __device__ __forceinline__ f32x4_t grad4(const OrthoSrc& s, int64_t at, int64_t n)

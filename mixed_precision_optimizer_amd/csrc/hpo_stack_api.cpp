@@ -217,6 +217,8 @@ hpo_status ns_scales(const hpo_muon_cfg* cfg, hpo::OrthoArgs& out)
         Pb *= std::max(Qb, 1e-6);
         S = std::max(next, 1e-6);
         ex = en;
+        if (!last)
+            out.lift_room = std::max(out.lift_room, static_cast<int32_t>(std::ceil(std::log2(Pb / S))));
     }
     out.p_exp = fit(Pb);
     /* P is held to 2^-22 of its bound: up to 2^11 of growth (the default coefficients' six

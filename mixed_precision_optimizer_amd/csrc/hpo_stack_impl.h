@@ -121,6 +121,7 @@ struct OrthoArgs {
     int64_t batch, rows, cols;
     MuonScalars sc;        /* gate, inv_scale, clip, momentum, eps */
     float x0_scale;        /* 2^ex of the first X */
+    int32_t lift_room;     /* log2 of the most that a X alone grows beyond the bounds of X's scales */
     NsStepScale step[HPO_NS_MAX_STEPS];
     void* ws;
 };

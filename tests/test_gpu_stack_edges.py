@@ -71,7 +71,8 @@ def test_rms_update_factors_beyond_fp32_leave_rows_of_zeros(S):
 # --------------------------------------------------------------------------
 # hpo_orthogonalize: norms far under ns_eps, or under fp32's normal numbers
 # --------------------------------------------------------------------------
-@pytest.mark.parametrize("r,c", [(40, 60), (60, 40), (90, 3000), (20000, 128)])
+@pytest.mark.parametrize("r,c", [(40, 60), (60, 40), (90, 3000), (20000, 128), (140, 150), (300, 520),
+                                 (520, 300), (1000, 1030), (2048, 2600)])
 @pytest.mark.parametrize("below", [1e-2, 1e-4, 1e-8, 1e-12, 1e-20, 1e-28])
 def test_orthogonalize_gradients_far_below_eps(S, r, c, below):
     """The iteration is all but linear there; its direction and size are as exact as anywhere else."""
@@ -81,7 +82,19 @@ def test_orthogonalize_gradients_far_below_eps(S, r, c, below):
     check_ortho(ortho(S, G.to(DEV)), G.double(), tag=f"norm {below} eps")
 
 
-@pytest.mark.parametrize("r,c", [(40, 60), (300, 20), (90, 3000)])
+@pytest.mark.parametrize("steps,coeffs", [(1, None), (7, None), (4, [(1.5, -0.5, 0.0)] * 4),
+                                          (3, [(8.2, -23.6, 17.3), (4.1, -2.9, 0.5), (1.875, -1.25, 0.375)])])
+@pytest.mark.parametrize("r,c", [(40, 60), (140, 300)])
+@pytest.mark.parametrize("below", [1e-3, 1e-5, 1e-9, 1e-15])
+def test_orthogonalize_schedules_far_below_eps(S, steps, coeffs, r, c, below):
+    """Schedules that grow X by more or less than the default; 1e-3 and 1e-5 lie where not all of them are scaled."""
+    G = gradient(119, 1, r, c)
+    G = G / torch.linalg.vector_norm(G) * 1e-7 * below
+    out = ortho(S, G.to(DEV), cfg=S.hpo.make_muon_cfg(ns_steps=steps, ns_coeffs=coeffs))
+    check_ortho(out, G.double(), steps, coeffs, tag=f"{steps} steps, norm {below} eps")
+
+
+@pytest.mark.parametrize("r,c", [(40, 60), (300, 20), (90, 3000), (140, 150), (300, 520)])
 @pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-7])
 @pytest.mark.parametrize("momentum", [False, True])
 def test_orthogonalize_subnormal_gradients(S, r, c, eps, momentum):
@@ -107,7 +120,7 @@ def test_orthogonalize_beyond_fp32_still_gives_zeros(S):
         assert bool((ortho(S, torch.full((1, r, c), 3e38, device=DEV)) == 0).all())
 
 
-@pytest.mark.parametrize("r,c", [(40, 300), (100, 3000)])
+@pytest.mark.parametrize("r,c", [(40, 300), (100, 3000), (140, 300), (1300, 5000)])
 def test_orthogonalize_far_below_eps_in_a_graph(S, r, c):
     """The exponent that such a matrix is held at belongs to each run of the graph."""
     G = gradient(115, 2, r, c).to(DEV)
