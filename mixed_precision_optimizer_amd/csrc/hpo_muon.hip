@@ -120,7 +120,7 @@ struct NsTile {
 /* Symmetric outputs (A = XX^T, B = bA + cAA^T) mirror whole tiles: square,
  * 1024 lanes, one workgroup per CU. */
 using SymTile = NsTile<4, 4, 2, 2, 64, 2, 1>;
-/* General outputs (X' = aX + BX and the last step) take SymTile.
+/* General outputs (X' = aX + BX and the last step) take SymTile; the stacks' always do.
  * HPO_NS_GEN_HALF = 1 selects 256 x 128 tiles of 512 lanes instead, two
  * workgroups per CU (k-stages of HPO_NS_GEN_BK in HPO_NS_GEN_STAGES
  * buffers), so that one workgroup's barriers and stores could overlap the
@@ -1436,7 +1436,7 @@ __device__ __forceinline__ int64_t lo_at_tile(int64_t i, int64_t j, int64_t np)
 
 __device__ __forceinline__ int64_t lo_at(int32_t tile, int64_t i, int64_t j, int64_t np)
 {
-    return tile == GenTile::kBM ? lo_at_tile<GenTile>(i, j, np)
+    return tile == SymTile::kBM ? lo_at_tile<SymTile>(i, j, np)
                                 : (tile == MidTile::kBM ? lo_at_tile<MidTile>(i, j, np) : lo_at_tile<SmallTile>(i, j, np));
 }
 
@@ -1583,7 +1583,7 @@ int64_t pad_to(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
 double launch_us(int64_t t, double wgs, double depth, bool general)
 {
     constexpr double kCus = 256.0;
-    if (t == GenTile::kBM)   /* one workgroup a CU: the general product's stores are not overlapped */
+    if (t == SymTile::kBM)   /* one workgroup a CU: the general product's stores are not overlapped */
         return 12.5 + (general ? 20.0 * std::min(1.0, wgs / kCus) : 0.0) + 0.0167 * depth * std::ceil(wgs / kCus);
     if (t == MidTile::kBM)
         return 7.0 + depth * (wgs <= kCus ? 0.0102 : 0.0085 * std::ceil(wgs / kCus));
@@ -1620,7 +1620,7 @@ double step_us(int64_t batch, int64_t m, int64_t n, int64_t t)
 
 int32_t pick_tile(int64_t batch, int64_t m, int64_t n)
 {
-    int32_t best = GenTile::kBM;
+    int32_t best = SymTile::kBM;
     for (int32_t t : {static_cast<int32_t>(MidTile::kBM), static_cast<int32_t>(SmallTile::kBM)})
         if (step_us(batch, m, n, t) < step_us(batch, m, n, best))
             best = t;
@@ -1771,9 +1771,8 @@ hipError_t ortho_slice(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64
 template <bool BF16>
 hipError_t ortho_tiles(const OrthoArgs& a, const OrthoPlan& p, int64_t z0, int64_t count, hipStream_t stream)
 {
-    static_assert(std::is_same_v<SymTile, GenTile>, "one padding for both kinds of product");
-    if (p.tile == GenTile::kBM)
-        return ortho_slice<BF16, GenTile>(a, p, z0, count, stream);
+    if (p.tile == SymTile::kBM)
+        return ortho_slice<BF16, SymTile>(a, p, z0, count, stream);
     if (p.tile == MidTile::kBM)
         return ortho_slice<BF16, MidTile>(a, p, z0, count, stream);
     return ortho_slice<BF16, SmallTile>(a, p, z0, count, stream);
