@@ -89,8 +89,12 @@ typedef struct {
  *     2^11 in growth): the iteration runs on the Gram matrix of X0 in 22-bit
  *     products and the long side is touched only at its ends; the norm is the
  *     root of the Gram matrix's trace.  Within about 5e-4 before the rounding.
- * Coefficients whose iteration may leave |X| <= 2^15 for a start of norm 1 are
- * refused (HPO_EINVAL).  A matrix that is all zero gives zeros, as does one whose
+ * Coefficients whose iteration may leave |X| <= 2^15 (or |X X^T|, |b A + c A A| <= 2^15)
+ * are refused (HPO_EINVAL).  The bound on the singular values starts at 1 and is
+ * widened by 1 % before every step, for the roundings: those of fp16 can all fall one
+ * way (equal elements), and coefficients that just hold on [0, 1] may multiply that by
+ * ten and more a step.  Such a schedule passes with its argument divided by 1.01:
+ * a / 1.01, b / 1.01^3, c / 1.01^5 for every step.  A matrix that is all zero gives zeros, as does one whose
  * norm is beyond fp32's largest value; one that holds an inf or NaN gives NaN everywhere.
  * The same inputs give the same bits.
  * With a non-zero *d_found_inf (nullable) nothing is written. */

@@ -192,12 +192,17 @@ hpo_status ns_scales(const hpo_muon_cfg* cfg, hpo::OrthoArgs& out)
     for (int32_t k = 0; k < cfg->ns_steps; ++k) {
         const double* c = cfg->ns_coeffs ? cfg->ns_coeffs + 3 * k : kDefault;
         const bool last = k + 1 == cfg->ns_steps;
-        /* 1 % for the roundings of the steps so far (more would leave the basin of the default
-         * coefficients, which grow without bound from s = 1.28 on) */
+        /* 1 % for the roundings of the steps so far: half a step of fp16 that falls one way everywhere
+         * is 2^-11 of s, times p'(s) (24 at s = 1 for steep first steps), times the next
+         * step's.  (More would leave the basin of the default coefficients, which grow without bound
+         * from s = 1.28 on.) */
         const double T = 1.01 * S, L = T * T, P = quadratic_max(c[1], c[2], L),
                      next = odd_quintic_max(c[0], c[1], c[2], T);
         if (!(next <= kMost) || !(P <= kMost) || !(L <= kMost))
-            return fail(HPO_EINVAL, "ns_coeffs: step %d may leave the range of the iteration (|X| up to %g)", k, next);
+            return fail(HPO_EINVAL,
+                        "ns_coeffs: step %d may leave the range of the iteration (|X| up to %g from a start of 1 widened by 1 %% a "
+                        "step)",
+                        k, next);
         const int ea = fit(L), eb = fit(P), en = last ? 0 : fit(next);
         hpo::NsStepScale& s = out.step[k];
         s.gram = static_cast<float>(std::ldexp(1.0, ea - 2 * ex));
