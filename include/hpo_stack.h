@@ -81,14 +81,19 @@ typedef struct {
  * scales that the host derives from the coefficients (bounds on X, A and B at
  * every step), accumulated in fp32.
  *   Short side over 128: the norm in binary64; what the rounding of X to fp16
- *     loses is kept beside it for the term a X of every step but the last, so that the small singular
- *     values, which grow by a each step, keep their accuracy.  Within about
- *     2e-3 (relative, Frobenius) of the exact iteration before the rounding to
- *     bf16.
+ *     loses is kept beside it for the term a X of every step but the last, so that the small
+ *     singular values, which grow by a each step, keep their accuracy.  With the default five
+ *     steps within 2e-3 (relative, Frobenius) of the exact iteration before the rounding to
+ *     bf16; within 4e-3 with other schedules that grow by up to 2^10 in all and six default
+ *     steps, 1e-2 with sixteen (3e-2 for short sides under 64).
  *   Short side up to 128 (unless the coefficients' steps multiply to more than
  *     2^11 in growth): the iteration runs on the Gram matrix of X0 in 22-bit
  *     products and the long side is touched only at its ends; the norm is the
- *     root of the Gram matrix's trace.  Within about 5e-4 before the rounding.
+ *     root of the Gram matrix's trace.  With the default five steps within 1e-3 before the
+ *     rounding (3e-3 for long sides of 5000 and more in stacks of hundreds, or of 10^6);
+ *     gradients without directions that stand out by ten and more: 2e-4.  What fp32 sums
+ *     lose of the Gram matrix grows by the square of the steps' growth: beside one
+ *     dominant direction 1e-2 at a growth of 2^10, 3e-2 with six default steps.
  * Coefficients whose iteration may leave |X| <= 2^15 (or |X X^T|, |b A + c A A| <= 2^15)
  * are refused (HPO_EINVAL).  The bound on the singular values starts at 1 and is
  * widened by 1 % before every step, for the roundings: those of fp16 can all fall one

@@ -698,19 +698,24 @@ __device__ __forceinline__ void iterate(const GramArgs& a, int64_t z, int wave, 
             __syncthreads();
         }
     }
-    /* P for the last pass: rows of 16-bit values, h then l (P is symmetric) */
+    /* P for the last pass: rows of 16-bit values, h then l.  Row by row as it is, not transposed:
+     * roundings leave P = Q_last ... Q_0 not quite symmetric, and what they put into the block that takes a strong
+     * direction of X0 to its small ones is grown by every later Q, the other block's by every
+     * earlier one, and only the first meets large elements of X0 (one direction over 0.1 % of
+     * noise: 1e-2 of the result with P^T, 2e-4 with P). */
     uint16_t* out = a.P + z * (2 * MP * MP);
     const float s = pow2f(a.p_exp - pq);
 #pragma unroll
     for (int j = 0; j < BN; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t h0, h1, l0, l1;
-            split2<1>(P[j][4 * q] * s, P[j][4 * q + 1] * s, h0, l0);
-            split2<1>(P[j][4 * q + 2] * s, P[j][4 * q + 3] * s, h1, l1);
-            const int at = col_of(j) * MP + lrow + 8 * q;
-            *reinterpret_cast<u32x2_t*>(out + at) = u32x2_t{h0, h1};
-            *reinterpret_cast<u32x2_t*>(out + MP * MP + at) = u32x2_t{l0, l1};
+        for (int r = 0; r < 16; r += 2) {
+            uint32_t h, l;
+            split2<1>(P[j][r] * s, P[j][r + 1] * s, h, l);
+            const int at = row_of(r) * MP + col_of(j);
+            out[at] = static_cast<uint16_t>(h & 0xffffu);
+            out[at + MP] = static_cast<uint16_t>(h >> 16);
+            out[MP * MP + at] = static_cast<uint16_t>(l & 0xffffu);
+            out[MP * MP + at + MP] = static_cast<uint16_t>(l >> 16);
         }
 }
 
