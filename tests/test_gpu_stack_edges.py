@@ -6,7 +6,8 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import stack_util as su  # noqa: E402
-from test_gpu_stack import CFG, DEV, S, check_ortho, check_rms, gen, gradient, ortho, workspace  # noqa: E402, F401
+from test_gpu_stack import (CFG, DEV, S, check_logits, check_ortho, check_rms, gen, gradient, ortho,  # noqa: E402, F401
+                            workspace)
 
 pytestmark = pytest.mark.gpu
 
@@ -135,3 +136,25 @@ def test_orthogonalize_far_below_eps_in_a_graph(S, r, c):
         torch.cuda.synchronize()
         assert torch.equal(got, su.bits(ortho(S, G))), size
         check_ortho(out, G.double().cpu(), tag=f"graph, size {size}")
+
+
+# --------------------------------------------------------------------------
+# hpo_qk_max_logits: what lies beside the heads
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("dim", [1, 3, 8, 16, 24, 32, 48, 57, 80, 100, 112, 136, 144, 160, 176, 191, 208, 224, 240, 248, 255])
+@pytest.mark.parametrize("pad", [0, 16, 9])
+def test_qk_max_does_not_see_what_lies_beside_a_head(S, dim, pad):
+    """NaN between the heads of a padded buffer, infinities behind a sequence's end, dims of every way into LDS."""
+    g = gen(dim * 3 + pad)
+    b, n, m, h = 2, 70, 331, 4
+    wide = lambda t, heads: torch.full((b, t, heads, dim + pad), math.nan, dtype=torch.bfloat16)   # noqa: E731
+    Q, K = wide(n, h), wide(m, 2)
+    q, k = torch.randn(b, n, h, dim, generator=g).bfloat16(), torch.randn(b, m, 2, dim, generator=g).bfloat16()
+    Q[..., :dim], K[..., :dim] = q, k
+    lens = torch.tensor([331, 200], dtype=torch.int32)
+    K[1, 200:, :, :dim] = math.inf
+    Q, K = Q.to(DEV), K.to(DEV)
+    for causal in (True, False):
+        out = torch.empty(h, device=DEV)
+        S.hpo_qk_max_logits(Q[..., :dim], K[..., :dim], out, 0.25, causal=causal, seqlens_k=lens.to(DEV))
+        check_logits(out, list(q), [k[0], k[1, :200]], 0.25, causal, -1, dim, f"dim {dim} pad {pad}")
