@@ -22,8 +22,8 @@
  *
  * Measured on 32 x 128 x 4096 fp32 with momentum (192 MB read and written in the first pass, 128 MB
  * read and 34 MB written in the last): gram 40 us (HBM: 5.6 TB/s with its partial results), their
- * sum 7 us, iterate 49 us (32 of 256 CUs, one matrix each; matrix cores busy 38 %: the splits
- * and barriers between its 17 products of 128^3 are the rest), apply 40 us.  The form with two
+ * sum 7 us, iterate 47 us (32 of 256 CUs, one matrix each; matrix cores busy 41 %: the splits
+ * and barriers between its 17 products of 128^3 are the rest), apply 39 us.  The form with two
  * products of the long side a step takes 1227 us there.  Tiny matrices (5 x 2 x 15) take 23 us,
  * a chain of latencies.
  *

@@ -1352,9 +1352,9 @@ hipError_t ns_step(const TensorDesc* d_desc, const MuonInfo* d_info, const MuonB
  * of the result for a low rank over 1 % of noise with either operand alone and 4e-4 with
  * both.  (Matrices with a short side up to 128 take hpo_gram.hip instead.)
  * Bound by the matrix cores at the clock they leave themselves; measured on 4096 x 14336
- * (4.33 ms in all): norm 57 us and input 95 us (HBM), Gram 247 us in three parts of its depth +
- * 33 us for their sum, A A^T 97 us, step 505 us (its epilogue moves 10 bytes per element), last
- * step 457 us.  3 x 1000 x 333: 17 launches of 6 to 9 us, 133 us. */
+ * (4.17 to 4.46 ms in all, from box to box; a trace of 4.45): norm 61 us and input 100 us (HBM), Gram
+ * 242 us in three parts of its depth + 33 us for their sum, A A^T 99 us, step 493 us (its epilogue moves 10
+ * bytes per element), last step 447 us.  3 x 1000 x 333: 17 launches of 7 to 10 us, 133 us. */
 constexpr int kSumThreads = 512;
 constexpr int64_t kSumMax = 512;      /* partial sums of squares per matrix, at most */
 constexpr int64_t kSumRun = 1024;     /* columns of one row that a wavefront takes at a time */
@@ -1472,8 +1472,8 @@ __global__ __launch_bounds__(kBlock) void k_stack_input(OrthoSrc s, const double
         const double norm = sqrt(tot), d64 = norm + static_cast<double>(s.sc.eps);
         lift = 0;
         if (norm > 0.0 && norm < kSmallShare * static_cast<double>(s.sc.eps)) {
-            const int32_t free = -1 - ilogb(norm / d64) - room;
-            lift = free > 0 ? free : 0;
+            const int32_t most = -1 - ilogb(norm / d64) - room;
+            lift = most > 0 ? most : 0;
         }
         up = lift;
         dnorm = static_cast<float>(norm) + s.sc.eps;
@@ -1579,7 +1579,10 @@ int64_t pad_to(int64_t x, int64_t a) { return (x + a - 1) / a * a; }
  * costs `fixed`, and a k of the products `alone` while the grid is resident at once, `full` a
  * workgroup per CU beyond.  Fitted to 19 shapes from 256 x 256 to 4096 x 4096 in stacks of
  * 1 to 64 on each tile, five steps each: 1 x 1024 x 1024 takes 461 / 283 / 164 us with
- * 256 / 128 / 64, 2 x 2048 x 2048 739 / 578 / 782, 1 x 4096 x 4096 1624 / 1856 / 2788. */
+ * 256 / 128 / 64, 2 x 2048 x 2048 739 / 578 / 782, 1 x 4096 x 4096 1624 / 1856 / 2788.
+ * It ranks tiles and is no forecast: the 256 tile's epilogue is charged once a launch, not once a round, so
+ * of several rounds it says too little (16 x 2048 x 1024: Gram 47, B 30, step 67 us, where a trace has
+ * 67, 46 and 123; the step of 4096 x 14336 306, where it takes 490). */
 double launch_us(int64_t t, double wgs, double depth, bool general)
 {
     constexpr double kCus = 256.0;

@@ -19,9 +19,12 @@
  * Measured: 8192 causal tokens, 32 heads over 8, dim 128, bf16: 206 to 216 us from box to box, 1.27
  * to 1.33 PFLOP/s of the seen pairs (a large library product reaches 1.20 here); the matrix cores are busy 65 % of the
  * cycles at the 1.85 GHz that this load leaves, LDS free of bank conflicts.  4096 tokens, 8 heads:
- * dim 64 17 us, 128 23 us, 192 30 us, 256 37 us; dims that are not multiples of 16 pass through
- * registers: 57 28 us.  Short sequences are bound by the two launches (about 9 us with
- * the binding).
+ * dim 64 18 us, 128 24 us, 192 32 us, 256 39 us.  Dims that are not multiples of 16 pass through
+ * registers and are bound by that (64-bit shifts beside the queries' fragments): 57 30 us,
+ * 72 36 us, 136 67 us, 200 98 us; over 192 they also spill (165 registers).  One or few queries: a head's
+ * workgroups each stage the keys of its group for one row in 64, so 4 x 1 on 9000 keys, 32 heads
+ * over 8, read 74 MB of keys in 38 us (16 at the rate of a large copy).  Short sequences
+ * are bound by the two launches (about 9 us with the binding).
  */
 #include <hip/hip_runtime.h>
 
@@ -441,8 +444,10 @@ hipError_t launch_qk_max(QkArgs a, bool fp16, bool aligned, hipStream_t stream)
     const int64_t tiles = static_cast<int64_t>(a.batch) * a.heads * a.q_tiles;
     /* Few query tiles: the keys are split until the chip's 512 resident workgroups have work, with
      * four stages each at the least.  Up to 64 queries keep one wavefront of a workgroup busy, and dims
-     * up to 128 leave room for a third one: 768 (4 x 1 query on 9000 keys, 32 heads over 8: 38 us, with
-     * 512 52, with 1024 55; longer queries lose 3 to 12 % with it). */
+     * up to 128 leave room for a third one: 768.  4 x 1 query on 9000 keys, 32 heads over 8, dim 128:
+     * 41 us, with 512 53, with 1024 55; over 14 shapes of 1 to 64 queries, 1 to 32 sequences, 2000 to
+     * 100000 keys, dims 40 to 128 it takes 0.55 to 0.92 of the time with 512 on ten, the same on three,
+     * and 1.14 on 64 queries of dim 64 (16 and 18 us).  Longer queries lose 3 to 12 % with it. */
     const int64_t wgs = a.max_q <= kWaveRows && a.dim <= 128 ? 768 : 512;
     const int64_t want = (wgs + tiles - 1) / tiles, most = (a.max_k + 4 * kTileK - 1) / (4 * kTileK);
     a.splits = static_cast<int32_t>(want < most ? want : most);

@@ -10,8 +10,9 @@
  * lies in eight neighbouring lanes.
  *
  * Measured: 4096 x 14336, bf16 O and weight: statistics 24 us (4.9 TB/s of O), update 108 us
- * (6.5 TB/s of its 12 bytes per element); 16 x 1024 x 2048 with 8-bit weights 16 and 58 us; 129 x 257:
- * 4 and 4 us, 11 us with the binding.  Clip of one layer (4096 x 4096 and 1024 x 4096
+ * (6.5 TB/s of its 12 bytes per element); 16 x 1024 x 2048 with 8-bit weights 16 and 59 us; 129 x 257:
+ * 4 and 4 us, 11 us with the binding.  Rows under 256 columns leave lanes of their piece idle: 65536 x 64
+ * takes 61 us (50 MB), 32768 x 128 38 us, 16384 x 256 26 us.  Clip of one layer (4096 x 4096 and 1024 x 4096
  * rows, nearly all clipped): 37 to 40 us, 5.3 to 5.7 TB/s.
  *
  * Floating point: built with -ffp-contract=off; every elementwise operation
