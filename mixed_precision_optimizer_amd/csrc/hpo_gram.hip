@@ -702,7 +702,7 @@ __device__ __forceinline__ void iterate(const GramArgs& a, int64_t z, int wave, 
      * roundings leave P = Q_last ... Q_0 not quite symmetric, and what they put into the block that takes a strong
      * direction of X0 to its small ones is grown by every later Q, the other block's by every
      * earlier one, and only the first meets large elements of X0 (one direction over 0.1 % of
-     * noise: 1e-2 of the result with P^T, 2e-4 with P). */
+     * noise: 1e-2 of the result with P^T, 4e-4 with P). */
     uint16_t* out = a.P + z * (2 * MP * MP);
     const float s = pow2f(a.p_exp - pq);
 #pragma unroll

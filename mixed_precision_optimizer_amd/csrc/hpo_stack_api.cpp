@@ -228,8 +228,8 @@ hpo_status ns_scales(const hpo_muon_cfg* cfg, hpo::OrthoArgs& out)
     out.p_exp = fit(Pb);
     /* What fp32 sums lose of S and A grows, in the directions of the small singular values, by the square of
      * the steps' growth.  Up to 2^11 (the default coefficients' six steps) it stays under 3e-2 where
-     * one direction is a thousand times the others, and under 1e-4 where none is ten times them: the two-product form
-     * has 6e-4 and 3.6e-3 there, at eight times the time (32 x 128 x 4096). */
+     * one direction is a thousand times the others, and under 5e-4 where none is ten times them: the
+     * two-product form has 6e-4 and 3.6e-3 there, at eight times the time (32 x 128 x 4096). */
     out.use_gram = Pb <= 2048.0 ? 1 : 0;
     return HPO_OK;
 }
