@@ -173,7 +173,9 @@ class StackMuon:
     nothing is read back.  The momentum, the row statistics, the orthogonalised
     update and the workspaces belong to the object: steps of one object are
     ordered on one stream, and a captured step is replayed only while the
-    object lives.
+    object lives.  What a checkpoint needs are `master`, `momentum` and `v`.
+    inv_scale is a host value and the skip a flag, as MixedPrecisionAdamW has them;
+    the scaler state that DeviceAdamW keeps on the device does not reach a step.
     """
 
     def __init__(self, master: torch.Tensor, param: Optional[torch.Tensor] = None,
