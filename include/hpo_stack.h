@@ -99,8 +99,9 @@ typedef struct {
  * widened by 1 % before every step, for the roundings: those of fp16 can all fall one
  * way (equal elements), and coefficients that just hold on [0, 1] may multiply that by
  * ten and more a step.  Such a schedule passes with its argument divided by 1.01:
- * a / 1.01, b / 1.01^3, c / 1.01^5 for every step.  A matrix that is all zero gives zeros, as does one whose
- * norm is beyond fp32's largest value; one that holds an inf or NaN gives NaN everywhere.
+ * a / 1.01, b / 1.01^3, c / 1.01^5 for every step.  A matrix that is all zero
+ * gives zeros, as does one whose norm (or an ns_eps that) is beyond fp32's largest value; one that
+ * holds an inf or NaN gives NaN everywhere.
  * The same inputs give the same bits.
  * With a non-zero *d_found_inf (nullable) nothing is written. */
 hpo_status hpo_orthogonalize(const hpo_stack* G, const hpo_stack* momentum, const hpo_stack* out,

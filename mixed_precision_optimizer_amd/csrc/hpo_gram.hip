@@ -575,8 +575,7 @@ __device__ __forceinline__ void iterate(const GramArgs& a, int64_t z, int wave, 
     const double id = d == 0.0 ? 0.0 : 1.0 / d;
     /* A norm far under eps leaves X0 far under 1, and its two fp16 values would keep few bits: X0 and
      * the result are held 2^lift larger (P does not depend on X0's scale). */
-    const int lift =
-        norm > 0.0 && norm < kSmallShare * static_cast<double>(a.s.sc.eps) ? -1 - ilogb(norm * id) : 0;
+    const int lift = far_below_eps(norm, a.s.sc.eps) ? -1 - ilogb(norm * id) : 0;
     /* the factor of A as a value in [1/2, 1) and an exponent */
     int fe = 0;
     const float fm = static_cast<float>(frexp(trace == 0.0 ? 0.0 : (unit * id) * (unit * id), &fe));

@@ -1471,7 +1471,7 @@ __global__ __launch_bounds__(kBlock) void k_stack_input(OrthoSrc s, const double
     if (tid == 0) {
         const double norm = sqrt(tot), d64 = norm + static_cast<double>(s.sc.eps);
         lift = 0;
-        if (norm > 0.0 && norm < kSmallShare * static_cast<double>(s.sc.eps)) {
+        if (far_below_eps(norm, s.sc.eps)) {
             const int32_t most = -1 - ilogb(norm / d64) - room;
             lift = most > 0 ? most : 0;
         }

@@ -9,6 +9,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <cfloat>
+
 #include "hpo_device.h"
 #include "hpo_stack_impl.h"
 
@@ -114,9 +116,12 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef f32x4_t f32x4_any __attribute__((aligned(4)));
 typedef u32x2_t u32x2_any __attribute__((aligned(2)));
 
-/* ||g~|| / eps below which X0 is held larger than it is: the iteration's cubic terms are
- * under 2^-18 of its linear ones there. */
-constexpr double kSmallShare = 0x1p-10;
+/* Where X0 is held larger than it is: under 2^-10 of eps the iteration's cubic terms are under
+ * 2^-18 of its linear ones.  An eps beyond fp32 came here as infinity and gives zeros. */
+__device__ __forceinline__ bool far_below_eps(double norm, float eps)
+{
+    return norm > 0.0 && eps <= FLT_MAX && norm < 0x1p-10 * static_cast<double>(eps);
+}
 
 /* Four consecutive stored elements: n of them are there (the others read as 0). */
 template <bool BF16>

@@ -121,6 +121,22 @@ def test_orthogonalize_beyond_fp32_still_gives_zeros(S):
         assert bool((ortho(S, torch.full((1, r, c), 3e38, device=DEV)) == 0).all())
 
 
+@pytest.mark.parametrize("r,c", [(40, 60), (90, 3000), (140, 150)])
+@pytest.mark.parametrize("eps", [1.0, 1e20, 3e38, 1e39, 1e300])
+def test_orthogonalize_large_eps(S, r, c, eps):
+    """An eps beyond fp32 is infinite to the library, as a norm would be: zeros.  Under it the result is what the
+    formula gives, down to bf16's subnormals (2^-133 apart)."""
+    G = gradient(121, 2, r, c)
+    out = ortho(S, G.to(DEV), cfg=S.hpo.make_muon_cfg(ns_eps=eps)).double().cpu()
+    if eps > 3.4e38:
+        assert bool((out == 0).all())
+        return
+    for z in range(2):
+        x, tol = su.ns_tolerance(G[z].double(), eps=float(torch.tensor(eps, dtype=torch.float32)))
+        d = float(torch.linalg.vector_norm(out[z] - x))
+        assert d <= tol * float(torch.linalg.vector_norm(x)) + 2.0 ** -134 * math.sqrt(r * c), (z, d)
+
+
 @pytest.mark.parametrize("r,c", [(40, 300), (100, 3000), (140, 300), (1300, 5000)])
 def test_orthogonalize_far_below_eps_in_a_graph(S, r, c):
     """The exponent that such a matrix is held at belongs to each run of the graph."""
