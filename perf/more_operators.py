@@ -1,0 +1,383 @@
+"""Cases of the model operators: what reads the weights that a step writes and
+adds to the main grads that the next step reads.
+
+A case is a dict of plain values with an "op":
+  embed       rows of the embedding table by token, scaled
+  embed_grad  their gradient added to the table's main grad
+  save        an activation kept in 8 bits with block scales
+  linear      product of a kept activation with an 8-bit weight
+  dgrad       gradient of that product's input
+  wgrad       gradient of its weight, added to the main grad
+
+`run` computes the plain form with elementary torch operations in fp32, or,
+where `own` is true, calls the library.  `exact` evaluates the definitions in
+binary64.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+F32, BF16, F16, F64 = torch.float32, torch.bfloat16, torch.float16, torch.float64
+DTYPES = {"fp32": F32, "bf16": BF16, "fp16": F16, "int32": torch.int32, "int64": torch.int64}
+SIZES = {"fp32": 4, "bf16": 2, "fp16": 2, "int32": 4, "int64": 8, "mx8": 1 + 1 / 32}
+MX_BLOCK = 32          # elements that share one power-of-two scale
+E4M3_MAX = 448.0
+GRAD_SCALE = 0.125     # eight micro-batches to a step
+SHARDS = 8             # of a table that is cut by vocabulary
+
+
+def listed():
+    return [
+        # The tokens of one long training sequence against an 8B model's table.
+        {"name": "embed_8k", "op": "embed", "tokens": 8192, "vocab": 128256, "cols": 4096, "first": -1,
+         "weight": "bf16", "out": "bf16", "ids": "int64"},
+        # A few tokens, a small odd table held in 8 bits: launches are what counts.
+        {"name": "embed_small_mx8", "op": "embed", "tokens": 17, "vocab": 1000, "cols": 333, "first": -1,
+         "weight": "mx8", "out": "fp32", "ids": "int32"},
+        # The gradient of the first, into the whole table's fp32 main grad.
+        {"name": "embed_grad_8k", "op": "embed_grad", "tokens": 8192, "vocab": 128256, "cols": 4096, "first": -1,
+         "dy": "bf16", "grad": "fp32", "ids": "int64"},
+        # The busiest of eight shards of that table, a global batch of tokens, odd width, bf16 main grads.
+        {"name": "embed_grad_shard", "op": "embed_grad", "tokens": 20000, "vocab": 16032, "cols": 1001, "first": 0,
+         "dy": "bf16", "grad": "bf16", "ids": "int32"},
+        # The MLP's inner activation of one sequence of an 8B model, kept for the backward pass.
+        {"name": "save_mlp", "op": "save", "batch": 1, "tokens": 8192, "cols": 14336, "x": "bf16", "pad": 0},
+        # A small odd one out of a padded fp32 buffer.
+        {"name": "save_small", "op": "save", "batch": 3, "tokens": 43, "cols": 257, "x": "fp32", "pad": 3},
+        # The up projection of an 8B model over one sequence.
+        {"name": "linear_mlp", "op": "linear", "batch": 1, "tokens": 8192, "cols": 4096, "rows": 14336, "y": "bf16",
+         "pad": 0},
+        # An expert layer in which every expert got few tokens.
+        {"name": "linear_experts", "op": "linear", "batch": 16, "tokens": 37, "cols": 2048, "rows": 1024, "y": "bf16",
+         "pad": 0},
+        # Input gradient of the up projection.
+        {"name": "dgrad_mlp", "op": "dgrad", "batch": 1, "tokens": 8192, "cols": 4096, "rows": 14336, "dy": "bf16",
+         "dx": "bf16", "pad": 0},
+        # Odd sizes in padded fp16 buffers: nothing is a multiple of a tile or of a vector.
+        {"name": "dgrad_odd", "op": "dgrad", "batch": 2, "tokens": 333, "cols": 1000, "rows": 577, "dy": "fp16",
+         "dx": "fp16", "pad": 5},
+        # Weight gradient of the up projection, added to the fp32 main grad.
+        {"name": "wgrad_mlp", "op": "wgrad", "batch": 1, "tokens": 8192, "cols": 4096, "rows": 14336, "dy": "bf16",
+         "grad": "fp32", "accumulate": True, "pad": 0},
+        # A key projection over eight sequences: the sum over the tokens is all there is to split.
+        {"name": "wgrad_long", "op": "wgrad", "batch": 1, "tokens": 65536, "cols": 1024, "rows": 1024, "dy": "bf16",
+         "grad": "bf16", "accumulate": False, "pad": 0},
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["embed", "embed_grad", "save", "linear", "dgrad", "wgrad"])
+    if op in ("embed", "embed_grad"):
+        while True:
+            n, v, c = _log_int(rng, 1, 65536), _log_int(rng, 8, 128256), _log_int(rng, 8, 8192)
+            if n * c <= 40_000_000 and v * c <= 200_000_000:
+                break
+        case = {"op": op, "tokens": n, "vocab": v, "cols": c, "first": rng.choice([-1, -1, 0, v]),
+                "ids": rng.choice(["int32", "int64"])}
+        if op == "embed":
+            case.update(weight=rng.choice(["bf16", "fp16", "fp32", "mx8"]), out=rng.choice(["bf16", "fp16", "fp32"]))
+        else:
+            case.update(dy=rng.choice(["bf16", "fp16", "fp32"]), grad=rng.choice(["fp32", "bf16"]))
+        return case
+    if op == "save":
+        while True:
+            b, t, c = _log_int(rng, 1, 32), _log_int(rng, 1, 20000), _log_int(rng, 1, 16000)
+            if 64 <= b * t * c <= 110_000_000:
+                break
+        return {"op": op, "batch": b, "tokens": t, "cols": c, "x": rng.choice(["bf16", "fp16", "fp32"]),
+                "pad": rng.choice([0, 0, 1, 8])}
+    while True:
+        b, t = _log_int(rng, 1, 32), _log_int(rng, 1, 32768)
+        c, r = _log_int(rng, 8, 16000), _log_int(rng, 8, 16000)
+        if b * t * c * r <= 300_000_000_000 and b * max(t * c, t * r, c * r) <= 100_000_000:
+            break
+    if rng.random() < 0.5:   # as most layers have them
+        c, r = -(-c // 64) * 64, -(-r // 64) * 64
+    case = {"op": op, "batch": b, "tokens": t, "cols": c, "rows": r, "pad": rng.choice([0, 0, 0, 1, 16])}
+    if op == "linear":
+        case.update(y=rng.choice(["bf16", "fp16", "fp32"]))
+    elif op == "dgrad":
+        case.update(dy=rng.choice(["bf16", "bf16", "fp16"]), dx=rng.choice(["bf16", "fp16", "fp32"]))
+    else:
+        case.update(dy=rng.choice(["bf16", "bf16", "fp16"]), grad=rng.choice(["fp32", "bf16"]),
+                    accumulate=rng.random() < 0.6)
+    return case
+
+
+# ---------------------------------------------------------------------------
+# inputs: from the seed alone
+# ---------------------------------------------------------------------------
+def _gen(seed):
+    return torch.Generator(device=DEV).manual_seed(int(seed))
+
+
+def _padded(x, pad):
+    """x as a view of a buffer whose rows are `pad` elements longer."""
+    if pad == 0:
+        return x.contiguous()
+    buf = torch.zeros(*x.shape[:-1], x.shape[-1] + pad, dtype=x.dtype, device=x.device)
+    buf[..., : x.shape[-1]] = x
+    return buf[..., : x.shape[-1]]
+
+
+def _mx_encode(w):
+    """(e4m3 values, e8m0 scales) of w's rows in blocks of 32: scale 2^(floor(log2 amax) - 8), values rounded to
+    nearest even and saturated at 448."""
+    c = w.shape[-1]
+    nb = -(-c // MX_BLOCK)
+    x = torch.nn.functional.pad(w, (0, nb * MX_BLOCK - c)).unflatten(-1, (nb, MX_BLOCK))
+    amax = x.abs().amax(-1)
+    e = torch.where(amax > 0, torch.frexp(amax)[1] - 1 - 8, -127).clamp(-127, 127)
+    q = torch.ldexp(x, -e.unsqueeze(-1)).clamp(-E4M3_MAX, E4M3_MAX).flatten(-2)[..., :c]
+    return q.to(torch.float8_e4m3fn), (e + 127).to(torch.uint8).view(torch.float8_e8m0fnu)
+
+
+def _total(case):
+    """Tokens the ids are drawn from: the table, or all of its shards."""
+    return case["vocab"] * (1 if case["first"] < 0 else SHARDS)
+
+
+def _ids(case, g):
+    """Token k about as often as 1 / (k + 1), as in text with tokens ranked by frequency."""
+    n = _total(case)
+    u = torch.rand(case["tokens"], generator=g, device=DEV, dtype=F64)
+    return (torch.exp(u * math.log(n + 1)).long() - 1).clamp(0, n - 1).to(DTYPES[case["ids"]])
+
+
+def _activation(g, *shape):
+    """Activations: some channels much larger than the others."""
+    return torch.randn(*shape, generator=g, device=DEV) * torch.exp(torch.randn(shape[-1], generator=g, device=DEV))
+
+
+def _inputs(case, seed):
+    g, op = _gen(seed), case["op"]
+    if op in ("embed", "embed_grad"):
+        n, v, c = case["tokens"], case["vocab"], case["cols"]
+        s = {"ids": _ids(case, g)}
+        if op == "embed":
+            w = 0.02 * torch.randn(v, c, generator=g, device=DEV)
+            if case["weight"] == "mx8":
+                s["w"], s["ws"] = _mx_encode(w)
+            else:
+                s["w"] = w.to(DTYPES[case["weight"]])
+        else:
+            s["dy"] = (1e-3 * torch.randn(n, c, generator=g, device=DEV)).to(DTYPES[case["dy"]])
+            s["grad"] = (1e-3 * torch.randn(v, c, generator=g, device=DEV)).to(DTYPES[case["grad"]])
+        return s
+    b, t, c = case["batch"], case["tokens"], case["cols"]
+    if op == "save":
+        return {"x": _padded(_activation(g, b, t, c).to(DTYPES[case["x"]]), case["pad"])}
+    r, s = case["rows"], {}
+    if op in ("linear", "wgrad"):
+        x, s["xs"] = _mx_encode(_activation(g, b, t, c).to(BF16).float())
+        s["x"] = _padded(x, case["pad"])
+    if op in ("linear", "dgrad"):
+        w, s["ws"] = _mx_encode(0.02 * torch.randn(b, r, c, generator=g, device=DEV))
+        s["w"] = _padded(w, case["pad"])
+    if op in ("dgrad", "wgrad"):
+        s["dy"] = _padded((1e-2 * torch.randn(b, t, r, generator=g, device=DEV)).to(DTYPES[case["dy"]]), case["pad"])
+    if op == "wgrad":
+        s["grad"] = (1e-2 * torch.randn(b, r, c, generator=g, device=DEV)).to(DTYPES[case["grad"]])
+    return s
+
+
+def prepare(case, seed):
+    s = {"case": case, **_inputs(case, seed)}
+    op = case["op"]
+    s["scale"] = math.sqrt(case["cols"]) if op == "embed" else GRAD_SCALE
+    s["first"] = max(0, case.get("first", 0))
+    if op == "embed":
+        s["out"] = torch.empty(case["tokens"], case["cols"], dtype=DTYPES[case["out"]], device=DEV)
+    elif op == "save":
+        b, t, c = case["batch"], case["tokens"], case["cols"]
+        s["q"] = torch.empty(b, t, c, dtype=torch.float8_e4m3fn, device=DEV)
+        s["qs"] = torch.empty(b, t, -(-c // MX_BLOCK), dtype=torch.uint8, device=DEV).view(torch.float8_e8m0fnu)
+    elif op == "linear":
+        s["y"] = torch.empty(case["batch"], case["tokens"], case["rows"], dtype=DTYPES[case["y"]], device=DEV)
+    elif op == "dgrad":
+        s["dx"] = torch.empty(case["batch"], case["tokens"], case["cols"], dtype=DTYPES[case["dx"]], device=DEV)
+    if own and op in ("embed_grad", "linear", "dgrad", "wgrad"):
+        from mixed_precision_optimizer_amd import hpo_model
+        if op == "embed_grad":
+            n = hpo_model.hpo_embedding_grad_workspace(s["ids"], s["grad"])
+        elif op == "linear":
+            n = hpo_model.hpo_mx8_linear_workspace(s["x"], s["w"])
+        elif op == "dgrad":
+            n = hpo_model.hpo_mx8_dgrad_workspace(s["dy"], s["w"])
+        else:
+            n = hpo_model.hpo_mx8_wgrad_workspace(s["dy"], s["x"])
+        s["work"] = torch.empty(n, dtype=torch.uint8, device=DEV)
+    return s
+
+
+# ---------------------------------------------------------------------------
+# one pass
+# ---------------------------------------------------------------------------
+def run(s):
+    return _run_own(s) if own else _run_plain(s)
+
+
+def _run_own(s):
+    from mixed_precision_optimizer_amd import hpo_model as hm
+    op = s["case"]["op"]
+    if op == "embed":
+        hm.hpo_embedding(s["ids"], s["w"], s["out"], scales=s.get("ws"), scale=s["scale"], first=s["first"])
+        return s["out"]
+    if op == "embed_grad":
+        hm.hpo_embedding_grad(s["ids"], s["dy"], s["grad"], s["work"], scale=s["scale"], first=s["first"])
+        return s["grad"]
+    if op == "save":
+        hm.hpo_mx8_save(s["x"], s["q"], s["qs"])
+        return {"q": s["q"], "qs": s["qs"]}
+    if op == "linear":
+        hm.hpo_mx8_linear(s["x"], s["xs"], s["w"], s["ws"], s["y"], s["work"])
+        return s["y"]
+    if op == "dgrad":
+        hm.hpo_mx8_dgrad(s["dy"], s["w"], s["ws"], s["dx"], s["work"])
+        return s["dx"]
+    hm.hpo_mx8_wgrad(s["dy"], s["x"], s["xs"], s["grad"], s["work"], scale=s["scale"],
+                     accumulate=s["case"]["accumulate"])
+    return s["grad"]
+
+
+def _mx_values(p, e):
+    """What 8-bit values and their block scales stand for, in fp32."""
+    f = torch.ldexp(torch.ones((), device=p.device), e.view(torch.uint8).int() - 127)
+    return p.float() * f.repeat_interleave(MX_BLOCK, -1)[..., : p.shape[-1]]
+
+
+def _run_plain(s):
+    case = s["case"]
+    op = case["op"]
+    if op in ("embed", "embed_grad"):
+        at = s["ids"].long() - s["first"]
+        inside = (at >= 0) & (at < case["vocab"])
+        at = torch.where(inside, at, 0)
+    if op == "embed":
+        rows = _mx_values(s["w"][at], s["ws"].view(torch.uint8)[at]) if "ws" in s else s["w"][at].float()
+        s["out"].copy_(torch.where(inside[:, None], rows * s["scale"], 0.0))
+        return s["out"]
+    if op == "embed_grad":
+        dy = torch.where(inside[:, None], s["dy"].float() * s["scale"], 0.0)
+        if case["grad"] == "fp32":
+            s["grad"].index_add_(0, at, dy)
+        else:
+            s["grad"].copy_(s["grad"].float().index_add_(0, at, dy))
+        return s["grad"]
+    if op == "save":
+        q, e = _mx_encode(s["x"].float())
+        s["q"].copy_(q)
+        s["qs"].copy_(e)
+        return {"q": s["q"], "qs": s["qs"]}
+    if op == "linear":
+        s["y"].copy_(_mx_values(s["x"], s["xs"]) @ _mx_values(s["w"], s["ws"]).mT.contiguous())
+        return s["y"]
+    if op == "dgrad":
+        s["dx"].copy_(s["dy"].float() @ _mx_values(s["w"], s["ws"]))
+        return s["dx"]
+    d = (s["dy"].float().mT.contiguous() @ _mx_values(s["x"], s["xs"])) * s["scale"]
+    s["grad"].copy_(s["grad"].float() + d if case["accumulate"] else d)
+    return s["grad"]
+
+
+# ---------------------------------------------------------------------------
+# what a pass cannot do without
+# ---------------------------------------------------------------------------
+def _share(lo, hi, total):
+    """Probability of a token in lo .. hi - 1."""
+    return math.log((hi + 1) / (lo + 1)) / math.log(total + 1)
+
+
+def _distinct(case):
+    """(tokens inside the table, different ones among them), as expected."""
+    n, total = case["tokens"], _total(case)
+    lo = max(0, case["first"])
+    hi, rows, k = lo + case["vocab"], 0.0, lo
+    while k < hi:   # runs of tokens of nearly one frequency
+        end = min(hi, max(k + 1, int(k * 1.02)))
+        rows += (end - k) * -math.expm1(-n * _share(k, end, total) / (end - k))
+        k = end
+    return n * _share(lo, hi, total), rows
+
+
+def work(case):
+    op = case["op"]
+    if op in ("embed", "embed_grad"):
+        n, c, idb = case["tokens"], case["cols"], SIZES[case["ids"]]
+        inside, rows = _distinct(case)
+        if op == "embed":
+            return {"bytes": n * idb + rows * c * SIZES[case["weight"]] + n * c * SIZES[case["out"]], "flops": inside * c}
+        return {"bytes": n * idb + inside * c * SIZES[case["dy"]] + 2 * rows * c * SIZES[case["grad"]],
+                "flops": (inside + 2 * rows) * c}
+    b, t, c = case["batch"], case["tokens"], case["cols"]
+    if op == "save":
+        return {"bytes": b * t * c * (SIZES[case["x"]] + SIZES["mx8"]), "flops": 2 * b * t * c}
+    r = case["rows"]
+    n = {"linear": t * c * SIZES["mx8"] + r * c * SIZES["mx8"] + t * r * SIZES[case.get("y", "fp32")],
+         "dgrad": t * r * SIZES[case.get("dy", "bf16")] + r * c * SIZES["mx8"] + t * c * SIZES[case.get("dx", "fp32")],
+         "wgrad": t * r * SIZES[case.get("dy", "bf16")] + t * c * SIZES["mx8"]
+         + r * c * SIZES[case.get("grad", "fp32")] * (2 if case.get("accumulate") else 1)}[op]
+    return {"bytes": b * n, "flops": 2 * b * t * c * r}
+
+
+# ---------------------------------------------------------------------------
+# the definitions in binary64
+# ---------------------------------------------------------------------------
+def _exact_values(p, e):
+    """value * 2^(byte - 127), block by block."""
+    v = p.to(F64)
+    power = torch.exp2(e.contiguous().view(torch.uint8).to(F64) - 127)
+    column = torch.arange(v.shape[-1], device=DEV) // MX_BLOCK
+    return v * power[..., column]
+
+
+def _exact_mx(x):
+    """Values and scales of x in blocks of 32, from the definition: the value nearest to x / 2^e on e4m3's grid."""
+    c = x.shape[-1]
+    nb = -(-c // MX_BLOCK)
+    y = torch.zeros(*x.shape[:-1], nb * MX_BLOCK, dtype=F64, device=DEV)
+    y[..., :c] = x
+    y = y.view(*x.shape[:-1], nb, MX_BLOCK)
+    amax = y.abs().max(-1).values
+    e = torch.where(amax > 0, torch.floor(torch.log2(torch.where(amax > 0, amax, 1.0))) - 8, -127.0).clamp(-127, 127)
+    y = y * torch.exp2(-e)[..., None]
+    # spacing of the grid at |y|: 2^(exponent - 3), from 2^-6 down 2^-9
+    step = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
+    y = (torch.round(y / step) * step).clamp(-E4M3_MAX, E4M3_MAX)
+    return y.reshape(*x.shape[:-1], nb * MX_BLOCK)[..., :c], torch.exp2(e)
+
+
+def exact(case, seed):
+    s, op = _inputs(case, seed), case["op"]
+    lo = max(0, case.get("first", 0))
+    if op == "embed":
+        w = _exact_values(s["w"], s["ws"]) if "ws" in s else s["w"].to(F64)
+        table = torch.cat([w, torch.zeros(1, case["cols"], dtype=F64, device=DEV)])   # a row for the ids outside
+        at = s["ids"].long() - lo
+        at[(at < 0) | (at >= case["vocab"])] = case["vocab"]
+        return torch.index_select(table, 0, at) * math.sqrt(case["cols"])
+    if op == "embed_grad":
+        seen = torch.nonzero((s["ids"] >= lo) & (s["ids"] < lo + case["vocab"]))[:, 0]
+        total = torch.zeros(case["vocab"], case["cols"], dtype=F64, device=DEV)
+        total.index_put_((s["ids"].long()[seen] - lo,), s["dy"].to(F64)[seen], accumulate=True)
+        return s["grad"].to(F64) + GRAD_SCALE * total
+    if op == "save":
+        q, e = _exact_mx(s["x"].to(F64))
+        return {"q": q, "qs": e}
+    out = []
+    for z in range(case["batch"]):
+        if op == "linear":
+            out.append(_exact_values(s["x"][z], s["xs"][z]) @ _exact_values(s["w"][z], s["ws"][z]).T)
+        elif op == "dgrad":
+            out.append(s["dy"][z].to(F64) @ _exact_values(s["w"][z], s["ws"][z]))
+        else:
+            d = GRAD_SCALE * (s["dy"][z].to(F64).T @ _exact_values(s["x"][z], s["xs"][z]))
+            out.append(d + s["grad"][z].to(F64) if case["accumulate"] else d)
+    return torch.stack(out)
