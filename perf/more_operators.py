@@ -102,7 +102,7 @@ def draw(rng):
         c, r = -(-c // 64) * 64, -(-r // 64) * 64
     case = {"op": op, "batch": b, "tokens": t, "cols": c, "rows": r, "pad": rng.choice([0, 0, 0, 1, 16])}
     if op == "linear":
-        case.update(y=rng.choice(["bf16", "fp16", "fp32"]))
+        case.update(y=rng.choice(["bf16", "fp16"]))
     elif op == "dgrad":
         case.update(dy=rng.choice(["bf16", "bf16", "fp16"]), dx=rng.choice(["bf16", "fp16", "fp32"]))
     else:
@@ -320,7 +320,7 @@ def work(case):
     if op == "save":
         return {"bytes": b * t * c * (SIZES[case["x"]] + SIZES["mx8"]), "flops": 2 * b * t * c}
     r = case["rows"]
-    n = {"linear": t * c * SIZES["mx8"] + r * c * SIZES["mx8"] + t * r * SIZES[case.get("y", "fp32")],
+    n = {"linear": t * c * SIZES["mx8"] + r * c * SIZES["mx8"] + t * r * SIZES[case.get("y", "bf16")],
          "dgrad": t * r * SIZES[case.get("dy", "bf16")] + r * c * SIZES["mx8"] + t * c * SIZES[case.get("dx", "fp32")],
          "wgrad": t * r * SIZES[case.get("dy", "bf16")] + t * c * SIZES["mx8"]
          + r * c * SIZES[case.get("grad", "fp32")] * (2 if case.get("accumulate") else 1)}[op]
