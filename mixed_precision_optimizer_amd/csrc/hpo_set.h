@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "hpo_muon_impl.h"
+#include "hpo_stack_impl.h"
 
 /* Event-pair timing of Muon launches (hpo_muon_profile_enable). */
 struct hpo_muon_prof {
@@ -122,6 +123,15 @@ hpo_status check_muon_step(hpo_set s, const hpo_muon_cfg* cfg, const hpo_group* 
 hpo_status muon_enqueue(hpo_set s, const hpo_muon_cfg* cfg, const hpo_group* groups, int32_t n_groups,
                         const hpo::MuonGate& gate, float inv_scale, double max_norm, const float* d_norm,
                         hipStream_t stream);
+
+/* hpo_stack_api.cpp: the rules of hpo_stack (shape, strides, alignment; dtypes are each call's own). */
+int64_t elem_size(int32_t dtype);
+bool is_empty(const hpo_stack* s);
+hpo_status check_stack(const hpo_stack* s, const char* what);
+/* check_stack, and the shape of `o`. */
+hpo_status check_like(const hpo_stack* s, const char* what, const hpo_stack* o, const char* other);
+/* What a kernel reads of a stack; strides over one matrix or row are 0. */
+hpo::StackView view(const hpo_stack* s);
 
 }  // namespace hpo_host
 

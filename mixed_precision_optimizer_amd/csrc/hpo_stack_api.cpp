@@ -18,6 +18,11 @@ constexpr int64_t kMaxBatch = 65535;              /* a launch's z dimension */
 constexpr int64_t kMaxRows = int64_t{1} << 24;    /* rows of a whole stack: one workgroup each, at most */
 constexpr int64_t kMaxSpan = int64_t{1} << 44;    /* elements between a stack's first and last */
 
+}  // namespace
+
+/* Stacks as every call that takes them checks them (hpo_set.h). */
+namespace hpo_host {
+
 int64_t elem_size(int32_t dtype) { return dtype == HPO_PARAM_FP32 ? 4 : (dtype == HPO_WEIGHT_MX8 ? 1 : 2); }
 
 bool is_empty(const hpo_stack* s) { return s->batch == 0 || s->rows == 0 || s->cols == 0; }
@@ -78,6 +83,10 @@ hpo::StackView view(const hpo_stack* s)
     }
     return v;
 }
+
+}  // namespace hpo_host
+
+namespace {
 
 /* Master and model weight of a row-wise update. */
 hpo_status weight_view(const hpo_stack* master, const hpo_stack* param, uint8_t* scales, hpo::WeightView& w)
