@@ -25,7 +25,7 @@ ARCH = "gfx950"
 
 # gfx950 kernel files and host files of libhpo
 DEVICE_SOURCES = ("hpo_kernels.hip", "hpo_muon.hip", "hpo_static.hip", "hpo_rows.hip", "hpo_qk.hip", "hpo_gram.hip",
-                  "hpo_embed.hip", "hpo_mx8.hip")
+                  "hpo_embed.hip", "hpo_mx8.hip", "hpo_mx8_grad.hip")
 HOST_SOURCES = ("hpo_api.cpp", "hpo_muon_api.cpp", "hpo_stack_api.cpp", "hpo_model_api.cpp")
 
 

@@ -81,6 +81,8 @@ struct ProductArgs {
 };
 
 int64_t product_workspace(ProductKind kind, int64_t batch, int64_t m, int64_t n, int64_t k);
+/* hpo_mx8_grad.hip: the tiles of dgrad and wgrad. */
+hipError_t launch_mx8_grad(bool wgrad, const ProductArgs& p, int32_t tile, bool direct, uint32_t grid, hipStream_t stream);
 hipError_t launch_product(ProductKind kind, ProductArgs a, hipStream_t stream);
 
 }  // namespace hpo
