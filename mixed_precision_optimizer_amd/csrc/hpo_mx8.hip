@@ -109,24 +109,26 @@ __global__ __launch_bounds__(kJoinThreads) void k_product_join(ProductArgs p)
  * (r, h) = (lane % 32, lane / 32) holds of row r bytes 16 h .. 16 h + 15 of the first block of 32 and
  * of the second, and the scale of block h.
  *
- * A stage of 128 elements of k is 2 TM groups of TN matrix instructions: groups 0 .. TM - 1 take the first
- * slice of 64, the others the second, group g the row block g % TM.  Fragments are read D groups ahead, across the
- * stage's end too: the barrier stands D groups before it, where the next stage must have landed and
- * nobody reads this one any more, so that the loads of the stage after it have a whole stage's time. */
+ * Slices of 64 k lie in a ring of four in LDS; one is TM groups of TN matrix instructions, and fragments are
+ * read D groups ahead, across the slice's end too.  A barrier stands D groups before that end, where the next slice
+ * must have landed and nobody reads this one any more: its place goes to the loads of the slice after next but
+ * one, so that a load has the time of three slices (with two whole stages of 128 in LDS, one ahead, the loop waits
+ * for loads: 8192 x 4096 x 14336 takes 467 us).  The loop's body is a stage of two slices, and the scale words are
+ * read once for both. */
 template <typename T, bool DIRECT>
 __global__ __launch_bounds__(T::kThreads) void k_mx8_linear(ProductArgs p)
 {
     constexpr int kRows = T::BM + T::BN;
-    constexpr int kStage = kRows * kRowBytes;
-    constexpr int kScales = 2 * kStage;              /* behind the stages: 16 scale bytes a row, twice */
+    constexpr int kSlice = kRows * kSliceBytes;
+    constexpr int kScales = 4 * kSlice;               /* behind the slices: 16 scale bytes a row, twice */
     constexpr int kScaleStage = kRows * 16;
-    constexpr int kChunks = kRows / 8 / T::kWaves;   /* 1 KB loads of a wavefront per stage: all of A or all of B */
-    constexpr int kPieces = kRows * 8 / T::kThreads;
+    constexpr int kChunks = kRows / 16 / T::kWaves;   /* 1 KB loads of a wavefront per slice: all of A or all of B */
+    constexpr int kPieces = kRows * 4 / T::kThreads;
     constexpr int kScaleRows = (kRows + T::kThreads - 1) / T::kThreads;
     constexpr int G = 2 * T::TM, D = T::TM > 1 ? 2 : 1, S = 2 * D;
-    static_assert((T::BM / 8) % kChunks == 0 && kChunks % 2 == 0, "a wavefront stages rows of one operand");
+    static_assert((T::BM / 16) % kChunks == 0, "a wavefront stages rows of one operand");
     static_assert(G % S == 0 && T::TM >= D, "fragment slots");
-    __shared__ __attribute__((aligned(16))) char lds[2 * kStage + 2 * kScaleStage];
+    __shared__ __attribute__((aligned(16))) char lds[4 * kSlice + 2 * kScaleStage];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int frow = lane & 31, fh = lane >> 5;
     const Work w = work_of(p);
@@ -138,7 +140,7 @@ __global__ __launch_bounds__(T::kThreads) void k_mx8_linear(ProductArgs p)
     const int64_t nb = (p.k + kMxBlock - 1) / kMxBlock;
     const uint8_t* SA = p.a_scales + (w.z * p.m + m0) * nb;
     const uint8_t* SB = p.b_scales + (w.z * p.n + n0) * nb;
-    const int steps = static_cast<int>((p.k + kRowBytes - 1) / kRowBytes);
+    const int steps = static_cast<int>((p.k + 127) / 128);
     const int k0 = static_cast<int>(static_cast<int64_t>(steps) * w.split / p.splits);
     const int k1 = static_cast<int>(static_cast<int64_t>(steps) * (w.split + 1) / p.splits);
 
@@ -147,84 +149,87 @@ __global__ __launch_bounds__(T::kThreads) void k_mx8_linear(ProductArgs p)
 
     /* straight into LDS: rows behind C's sides lie behind the descriptor's end, or (a lone row, stride
      * 0) hold copies of it */
-    const bool side_b = wave * kChunks >= T::BM / 8;
+    const bool side_b = wave * kChunks >= T::BM / 16;
     __amdgpu_buffer_rsrc_t rs;
-    int ld = 0, voff[2] = {0, 0}, piece[2] = {0, 0};
+    int ld = 0, voff = 0;
+    const int piece = ((lane & 3) ^ slice_swizzle(lane >> 2)) * 16;
     u32x4_t held[DIRECT ? 1 : kPieces];
     if constexpr (DIRECT) {
         ld = static_cast<int>(side_b ? p.b_rs : p.a_rs);
         rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(side_b ? B : A), 0,
                                                static_cast<int>(((side_b ? rows_n : rows_m) - 1) * ld + p.k), 0x00020000);
-        const int r0 = wave * kChunks * 8 - (side_b ? T::BM : 0) + (lane >> 3);
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            piece[c] = (lane & 7) ^ row_swizzle(8 * c + (lane >> 3));
-            voff[c] = r0 * ld + piece[c] * 16;
-        }
+        voff = (wave * kChunks * 16 - (side_b ? T::BM : 0) + (lane >> 2)) * ld + piece;
     }
-    auto fetch = [&](int kt, int buf) {
-        const int64_t left = p.k - static_cast<int64_t>(kt) * kRowBytes;   /* bytes of the row from here */
+    /* Loads first .. last - 1 of slice x, which goes to place `to`.  Slices behind the last are fetched too, as
+     * zeros from nowhere: the loads in flight stay as many. */
+    auto fetch = [&](int x, int to, int first, int last) {
+        const int64_t k = static_cast<int64_t>(x) * 64, left = p.k - k;   /* bytes of the row from here */
         if constexpr (DIRECT) {
-            int v[2] = {voff[0], voff[1]};
-            if (left < kRowBytes) {
+            const int v = left >= 64 || piece < left ? voff : kNowhere, soff = left > 0 ? static_cast<int>(k) : 0;
 #pragma unroll
-                for (int c = 0; c < 2; ++c)
-                    v[c] = piece[c] * 16 < left ? v[c] : kNowhere;
-            }
-#pragma unroll
-            for (int c = 0; c < kChunks; ++c)
-                buffer_load_lds16(rs, lds + buf * kStage + (wave * kChunks + c) * 1024, v[c & 1], kt * kRowBytes + c * 8 * ld);
+            for (int c = first; c < last; ++c)
+                buffer_load_lds16(rs, lds + to * kSlice + (wave * kChunks + c) * 1024, v, soff + c * 16 * ld);
         } else {
 #pragma unroll
             for (int c = 0; c < kPieces; ++c) {
-                const int i = c * T::kThreads + tid, r = i >> 3, at = (i & 7) * 16;
+                const int i = c * T::kThreads + tid, r = i >> 2, at = (i & 3) * 16;
                 const uint8_t* row = r < T::BM ? A + clamp(r) * p.a_rs : B + clamp(r) * p.b_rs;
-                held[c] = load16(row + static_cast<int64_t>(kt) * kRowBytes + at, left - at);
+                held[c] = load16(row + k + at, left - at);
             }
         }
     };
-    auto put = [&](int buf) {
+    auto put = [&](int to) {
         if constexpr (!DIRECT) {
 #pragma unroll
             for (int c = 0; c < kPieces; ++c) {
                 const int i = c * T::kThreads + tid;
-                *reinterpret_cast<u32x4_t*>(lds + buf * kStage + piece_at(i >> 3, i & 7)) = held[c];
+                *reinterpret_cast<u32x4_t*>(lds + to * kSlice + slice_at(i >> 2, i & 3)) = held[c];
             }
         }
     };
+    /* The next slice has landed: the two behind it may still be in flight. */
+    auto arrive = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(waitcnt(DIRECT ? 2 * kChunks : 63));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
     /* Scales of four stages at a time; a byte behind the row's end reads as 0, never as a neighbour's NaN.
-     * A row of fewer than 16 has only the first four stages'; longer ones read their last 16 at their end. */
+     * A row of fewer than 16 has only the first stages'; longer ones read their last 16 at their end. */
     u32x4_t sheld[kScaleRows];
     const uint8_t* srow[kScaleRows];
+    int late = 0;   /* bits that the held scales lie too early */
 #pragma unroll
     for (int c = 0; c < kScaleRows; ++c) {
         const int r = c * T::kThreads + tid;
         srow[c] = (r < T::BM ? SA : SB) + clamp(r < kRows ? r : 0) * nb;
     }
-    auto fetch_scales = [&](int64_t at) {   /* 16 < nb */
-        const int64_t start = at < nb - 16 ? at : nb - 16;
+    auto fetch_scales = [&](int64_t at) {
+        if (nb >= 16) {
+            const int64_t start = at < nb - 16 ? at : nb - 16;
+            late = at - start < 16 ? static_cast<int>(at - start) * 8 : 0;   /* 16 and more: behind the last stage */
 #pragma unroll
-        for (int c = 0; c < kScaleRows; ++c)
-            sheld[c] = *reinterpret_cast<const u32x4_any*>(srow[c] + start);
-        if (start < at) {
-            const int by = static_cast<int>(at - start) * 8;
+            for (int c = 0; c < kScaleRows; ++c)
+                sheld[c] = *reinterpret_cast<const u32x4_any*>(srow[c] + start);
+        }
+    };
+    auto put_scales = [&](int at) {
+        if (late > 0) {
 #pragma unroll
             for (int c = 0; c < kScaleRows; ++c) {
                 uint64_t lo = sheld[c][0] | (static_cast<uint64_t>(sheld[c][1]) << 32);
                 uint64_t hi = sheld[c][2] | (static_cast<uint64_t>(sheld[c][3]) << 32);
-                lo = by < 64 ? (lo >> by) | (hi << (64 - by)) : hi >> (by - 64);
-                hi = by < 64 ? hi >> by : 0;
+                lo = late < 64 ? (lo >> late) | (hi << (64 - late)) : hi >> (late - 64);
+                hi = late < 64 ? hi >> late : 0;
                 sheld[c] = u32x4_t{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
                                    static_cast<uint32_t>(hi >> 32)};
             }
         }
-    };
-    auto put_scales = [&](int buf) {
 #pragma unroll
         for (int c = 0; c < kScaleRows; ++c) {
             const int r = c * T::kThreads + tid;
-            if (r < kRows)
-                *reinterpret_cast<u32x4_t*>(lds + kScales + buf * kScaleStage + r * 16) = sheld[c];
+            if (kRows % T::kThreads == 0 || r < kRows)
+                *reinterpret_cast<u32x4_t*>(lds + at + r * 16) = sheld[c];
         }
     };
 
@@ -235,26 +240,25 @@ __global__ __launch_bounds__(T::kThreads) void k_mx8_linear(ProductArgs p)
         for (int j = 0; j < T::TN; ++j)
             acc[i][j] = f32x16_t{};
     const int am = wave / T::WN * (T::TM * 32) + frow, bn = T::BM + wave % T::WN * (T::TN * 32) + frow;
-    /* Piece 4 s + fh (+ 2) of a lane's row lies at its piece fh's offset with bits 6 and 5 turned over.  The offsets
-     * pass through an empty asm every stage: else the compiler keeps all sixteen of them, and spills. */
-    const int base_a = piece_at(am, fh), base_b = piece_at(bn, fh);
+    /* pieces fh and 2 + fh of a lane's row: the second at the first's offset with bit 5 turned over */
+    const int base_a = slice_at(am, fh), base_b = slice_at(bn, fh);
     auto frag = [&](int base, int block, int s) {
-        const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(lds + (base ^ (s << 6)) + block * (32 * kRowBytes));
-        const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(lds + (base ^ (s << 6) ^ 32) + block * (32 * kRowBytes));
+        const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(lds + base + s * kSlice + block * (32 * kSliceBytes));
+        const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(lds + (base ^ 32) + s * kSlice + block * (32 * kSliceBytes));
         return i32x8_t{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]), static_cast<int>(lo[3]),
                        static_cast<int>(hi[0]), static_cast<int>(hi[1]), static_cast<int>(hi[2]), static_cast<int>(hi[3])};
     };
     i32x8_t fa[S], fb[2][T::TN];
-    int sa[T::TM], sb[T::TN], na[T::TM], nbs[T::TN];
-    /* the scale words of stage `at` from the first: block h of a slice of 64 in byte 2 * slice */
-    auto read_scales = [&](int at) {
-        const char* scl = lds + kScales + ((at >> 2) & 1) * kScaleStage + (at & 3) * 4;
+    int sa[T::TM], sb[T::TN], na[T::TM], nb4[T::TN];
+    /* the scale words of stage `at` from the first: block h of slice s in byte 2 s */
+    auto read_scales = [&](unsigned at) {
+        const char* scl = lds + kScales + (at >> 2 & 1) * kScaleStage + (at & 3) * 4;
 #pragma unroll
         for (int i = 0; i < T::TM; ++i)
             na[i] = static_cast<int>(*reinterpret_cast<const uint32_t*>(scl + (am + 32 * i) * 16) >> (8 * fh));
 #pragma unroll
         for (int j = 0; j < T::TN; ++j)
-            nbs[j] = static_cast<int>(*reinterpret_cast<const uint32_t*>(scl + (bn + 32 * j) * 16) >> (8 * fh));
+            nb4[j] = static_cast<int>(*reinterpret_cast<const uint32_t*>(scl + (bn + 32 * j) * 16) >> (8 * fh));
     };
     auto take_scales = [&]() {
 #pragma unroll
@@ -262,87 +266,94 @@ __global__ __launch_bounds__(T::kThreads) void k_mx8_linear(ProductArgs p)
             sa[i] = na[i];
 #pragma unroll
         for (int j = 0; j < T::TN; ++j)
-            sb[j] = nbs[j];
-    };
-
-    int here_a = 0, here_b = 0;
-    auto look = [&](int buf) {
-        here_a = base_a + buf * kStage;
-        here_b = base_b + buf * kStage;
-        asm volatile("" : "+v"(here_a), "+v"(here_b));
-    };
-    /* MORE: another stage follows */
-    auto stage = [&](int kt, auto MORE) {
-        constexpr bool more = decltype(MORE)::value;
-        const int at = kt - k0, buf = at & 1;
-        look(buf);
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            if constexpr (more) {
-                if (g == G - D) {
-                    put(buf ^ 1);
-                    land();
-                    if (kt + 2 < k1)
-                        fetch(kt + 2, buf);
-                    /* a group of four's scales are fetched in its second stage and put down in the third */
-                    if ((at & 3) == 1 && kt + 3 < k1)
-                        fetch_scales(4 * static_cast<int64_t>(kt + 3));
-                    if ((at & 3) == 2 && kt + 2 < k1)
-                        put_scales(((at >> 2) & 1) ^ 1);
-                    read_scales(at + 1);
-                    look(buf ^ 1);
-#pragma unroll
-                    for (int j = 0; j < T::TN; ++j)
-                        fb[0][j] = frag(here_b, j, 0);
-                }
-            }
-            if (g + D < G || more)
-                fa[(g + D) % S] = frag(here_a, (g + D) % T::TM, (g + D) % G / T::TM);
-            if (g == T::TM - D) {
-#pragma unroll
-                for (int j = 0; j < T::TN; ++j)
-                    fb[1][j] = frag(here_b, j, 1);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-            const int i = g % T::TM;
-#pragma unroll
-            for (int j = 0; j < T::TN; ++j) {
-                if (g < T::TM)
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[0][j], fa[g % S], acc[i][j], 0, 0, 0, sb[j],
-                                                                                0, sa[i]);
-                else
-                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[1][j], fa[g % S], acc[i][j], 0, 0, 2, sb[j],
-                                                                                2, sa[i]);
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        if constexpr (more)
-            take_scales();
+            sb[j] = nb4[j];
     };
     if (k0 < k1) {
 #pragma unroll
         for (int c = 0; c < kScaleRows; ++c)
             sheld[c] = load16(srow[c] + 4 * static_cast<int64_t>(k0), nb - 4 * static_cast<int64_t>(k0));
-        fetch(k0, 0);
-        put_scales(0);
-        put(0);
-        land();
-        if (k0 + 1 < k1)
-            fetch(k0 + 1, 1);
+        if constexpr (DIRECT) {
+#pragma unroll
+            for (int x = 0; x < 3; ++x)
+                fetch(2 * k0 + x, x, 0, kChunks);
+            put_scales(kScales);
+            arrive();
+            fetch(2 * k0 + 3, 3, 0, kChunks * D / T::TM);
+        } else {
+            fetch(2 * k0, 0, 0, 0);
+            put_scales(kScales);
+            put(0);
+            arrive();
+            fetch(2 * k0 + 1, 1, 0, 0);
+        }
         read_scales(0);
         take_scales();
-        look(0);
 #pragma unroll
         for (int j = 0; j < T::TN; ++j)
-            fb[0][j] = frag(here_b, j, 0);
+            fb[0][j] = frag(base_b, j, 0);
 #pragma unroll
         for (int g = 0; g < D; ++g)
-            fa[g] = frag(here_a, g % T::TM, g / T::TM);
-        int kt = k0;
-        for (; kt + 1 < k1; ++kt)
-            stage(kt, std::true_type{});
-        stage(kt, std::false_type{});
+            fa[g] = frag(base_a, g % T::TM, g / T::TM);
+        for (int kt = k0; kt < k1; ++kt) {
+            const unsigned at = static_cast<unsigned>(kt - k0);
+            const int pair = static_cast<int>(at & 1) * 2;   /* places pair, pair + 1 of the ring */
+            int here_a = base_a + pair * kSlice, here_b = base_b + pair * kSlice;
+            /* not to be kept for both halves of the ring in registers that the sums need */
+            asm volatile("" : "+v"(here_a), "+v"(here_b));
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int slice = g / T::TM;
+                if (g % T::TM == T::TM - D) {
+                    put(slice == 0 ? pair + 1 : pair ^ 2);
+                    arrive();
+                    if constexpr (!DIRECT)
+                        fetch(2 * kt + 2 + slice, 0, 0, 0);
+                    if (slice == 1) {
+                        /* four stages' scales are fetched in the second of the four before and put down in the third */
+                        if ((at & 3) == 1)
+                            fetch_scales(4 * static_cast<int64_t>(kt + 3));
+                        if ((at & 3) == 2)
+                            put_scales(kScales + ((at >> 2 & 1) ^ 1) * kScaleStage);
+                        read_scales(at + 1);
+                        here_a = base_a + (pair ^ 2) * kSlice;
+                        here_b = base_b + (pair ^ 2) * kSlice;
+                        asm volatile("" : "+v"(here_a), "+v"(here_b));
+                    }
+                }
+                const int h = (g + D) % G, s = h / T::TM;
+                if constexpr (DIRECT) {
+                    /* a group's share of the loads: all at once they would keep every wavefront from its products
+                     * until the last is taken.  Before slice 0's barrier they are still those of the stage before. */
+                    const int q = h % T::TM;
+                    const int first = q * kChunks / T::TM, last = (q + 1) * kChunks / T::TM, freed = (g + D - T::TM) / T::TM;
+                    if (g < T::TM - D)
+                        fetch(2 * kt + 3, pair ^ 3, first, last);
+                    else
+                        fetch(2 * kt + 4 + freed, pair + freed, first, last);
+                }
+                if (h % T::TM == 0) {
+#pragma unroll
+                    for (int j = 0; j < T::TN; ++j)
+                        fb[s][j] = frag(here_b, j, s);
+                }
+                fa[(g + D) % S] = frag(here_a, h % T::TM, s);
+                __builtin_amdgcn_sched_barrier(0);
+                const int i = g % T::TM;
+#pragma unroll
+                for (int j = 0; j < T::TN; ++j) {
+                    if (slice == 0)
+                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[0][j], fa[g % S], acc[i][j], 0, 0, 0,
+                                                                                    sb[j], 0, sa[i]);
+                    else
+                        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fb[1][j], fa[g % S], acc[i][j], 0, 0, 2,
+                                                                                    sb[j], 2, sa[i]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            take_scales();
+        }
     }
+    land();
     epilogue<T, false>(p, w, lds, acc);
 }
 
@@ -378,7 +389,7 @@ Cut cut_of(ProductKind kind, int64_t batch, int64_t m, int64_t n, int64_t k)
 {
     constexpr int64_t kCus = 256;
     Cut c{};
-    const int64_t steps = (k + (kind == kLinear ? kRowBytes : kStepK) - 1) / (kind == kLinear ? kRowBytes : kStepK);
+    const int64_t depth = kind == kLinear ? 128 : kStepK, steps = (k + depth - 1) / depth;
     for (int t : {256, 128, 64}) {
         c.tile = t;
         c.tiles_m = (m + t - 1) / t;

@@ -7,6 +7,8 @@
 #ifndef HPO_PRODUCT_DEVICE_H
 #define HPO_PRODUCT_DEVICE_H
 
+#include <type_traits>
+
 #include "hpo_model_device.h"
 
 namespace hpo {
@@ -80,6 +82,11 @@ constexpr int kNowhere = 0x7ffffff0;   /* an offset behind every descriptor's en
 __device__ __forceinline__ int row_swizzle(int r) { return (r & 7) ^ ((r >> 3) & 1); }
 __device__ __forceinline__ int piece_at(int r, int p) { return r * kRowBytes + ((p ^ row_swizzle(r)) << 4); }
 
+/* The same for slices of 64 bytes a row. */
+constexpr int kSliceBytes = 64;
+__device__ __forceinline__ int slice_swizzle(int r) { return (r >> 2) & 3; }
+__device__ __forceinline__ int slice_at(int r, int p) { return r * kSliceBytes + ((p ^ slice_swizzle(r)) << 4); }
+
 /* Rows that run along C's side (W elements of 16 bits, one row per k): their 32-byte pairs of pieces are
  * permuted by the row, so that the four rows (twice) a transposing read takes 32 bytes each of lie in
  * distinct banks. */
@@ -103,12 +110,15 @@ __device__ __forceinline__ u32x4_t load16(const uint8_t* at, int64_t left)
     return v;
 }
 
+/* s_waitcnt's operand (gfx9 encoding): at most `loads` in flight, no LDS access. */
+constexpr int waitcnt(int loads) { return (loads & 15) | 0x70 | (loads >> 4) << 14; }
+
 /* Waits for this wavefront's loads and LDS accesses, then for the workgroup.  Nothing else makes
  * loads into LDS land before the barrier. */
 __device__ __forceinline__ void land()
 {
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0x0070);   /* gfx9 encoding: vmcnt(0) lgkmcnt(0) */
+    __builtin_amdgcn_s_waitcnt(waitcnt(0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
 }
