@@ -8,7 +8,7 @@
  *
  * The gradient adds rows of dY that belong to one token.  Atomics on the main grad would leave
  * the order of the sums to chance and pass over G once per token, so the tokens are sorted
- * first (stable, by radix: equal tokens stay in order of position) and the sorted list is cut into
+ * first (stable: equal tokens stay in order of position) and the sorted list is cut into
  * slabs of equal length, one per group of lanes and column piece: the work is even however often a
  * token comes.  A run of equal tokens inside a slab goes straight into its row of G, each row read and
  * written once; a run that crosses a slab's border leaves its parts in the workspace, and a last
@@ -16,8 +16,6 @@
  * token of its kind adds up the others.
  */
 #include <hip/hip_runtime.h>
-
-#include <algorithm>
 
 #include "hpo_model_device.h"
 
@@ -34,8 +32,8 @@ __device__ __forceinline__ int64_t id_at(const void* ids, int id64, int64_t t)
 /* Row of the table, or -1. */
 __device__ __forceinline__ int64_t row_of(const void* ids, int id64, int64_t t, int64_t first, int64_t rows)
 {
-    const int64_t id = id_at(ids, id64, t);
-    return id >= first && id - first < rows ? id - first : -1;
+    const uint64_t d = static_cast<uint64_t>(id_at(ids, id64, t)) - static_cast<uint64_t>(first);
+    return d < static_cast<uint64_t>(rows) ? static_cast<int64_t>(d) : -1;
 }
 
 /* Eight weights of a row in fp32. */
@@ -102,8 +100,6 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 constexpr int kDigitBits = 11;                 /* of a pass, at most; keys have 22 at most */
 constexpr int kBins = 1 << kDigitBits;
-constexpr int kOneItems = 8;                   /* tokens of a lane where one workgroup sorts them all */
-constexpr int kOneMax = kSortThreads * kOneItems;
 constexpr int kBlockItems = 4;                 /* where many do */
 constexpr int kBlockTokens = kSortThreads * kBlockItems;
 
@@ -205,52 +201,159 @@ __device__ __forceinline__ int32_t key_of(const EmbedGradArgs& a, int64_t t)
     return static_cast<int32_t>(row < 0 ? a.rows : row);
 }
 
-/* The whole sort in one workgroup. */
-__global__ __launch_bounds__(kSortThreads) void k_sort_one(EmbedGradArgs a, Sorted s, int bits0, int bits1)
+/* One launch for up to kBucketMax tokens: workgroup b looks through all of them for the rows with row mod
+ * gridDim.x = b, which are its part of the list (behind those of the buckets before it), collects them in
+ * order of position, and sorts them by the rest of the row.  So equal rows come together, though not in
+ * their order; ids without a row come last. */
+constexpr int kBucketThreads = 1024;
+constexpr int kBucketWaves = kBucketThreads / 64;
+constexpr int kBucketMax = 65536;
+constexpr int kBucketBins = 2048;   /* rests of a row */
+constexpr int kBucketHold = 16;     /* tokens of a lane that are kept between the two looks */
+
+__global__ __launch_bounds__(kBucketThreads) void k_sort_bucket(EmbedGradArgs a, Sorted s, int shift)
 {
-    __shared__ DigitLds lds;
-    __shared__ int32_t keys[kOneMax];
-    __shared__ uint16_t toks[kOneMax];
+    __shared__ uint32_t count[kBucketWaves][kBucketBins];
+    __shared__ uint32_t wave_in[kBucketWaves], wave_below[kBucketWaves], wave_rows[kBucketWaves];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, n = static_cast<int>(a.n);
-    int32_t key[kOneItems], tok[kOneItems];
-    uint32_t valid = 0, rank[kOneItems];
-    /* lanes take as few tokens each as there are: the wavefronts behind the last one have none */
-    const int at0 = wave * 64 * kOneItems + lane;
+    const uint32_t bucket = blockIdx.x, mask = (1u << shift) - 1u;
+    const int bins = static_cast<int>((a.rows - 1) >> shift) + 1;
+    const int chunks = (n + 64 * kBucketWaves - 1) / (64 * kBucketWaves), first = wave * chunks * 64 + lane;
+    const int32_t none = static_cast<int32_t>(a.rows);
+    int32_t held[kBucketHold];
+    uint32_t in = 0, below = 0, listed = 0;
+    auto look = [&](int32_t key) {
+        const uint32_t r = static_cast<uint32_t>(key) & mask;
+        in += __builtin_popcountll(__ballot(key < none && r == bucket));
+        below += __builtin_popcountll(__ballot(key < none && r < bucket));
+        listed += __builtin_popcountll(__ballot(key < none));
+    };
 #pragma unroll
-    for (int i = 0; i < kOneItems; ++i) {
-        tok[i] = at0 + 64 * i;
-        const bool in = tok[i] < n;
-        valid |= static_cast<uint32_t>(in) << i;
-        key[i] = in ? key_of(a, tok[i]) : 0;
+    for (int c = 0; c < kBucketHold; ++c) {
+        const int t = first + 64 * c;
+        held[c] = c < chunks && t < n ? key_of(a, t) : none;
     }
-    for (int pass = 0; pass < (bits1 > 0 ? 2 : 1); ++pass) {
-        const int shift = pass ? bits0 : 0, bits = pass ? bits1 : bits0;
-        rank_digits<kOneItems>(lds, key, valid, shift, bits, rank);
-        scan_bins(lds, 1 << bits);
-        const bool last = pass == (bits1 > 0 ? 1 : 0);
 #pragma unroll
-        for (int i = 0; i < kOneItems; ++i)
-            if ((valid >> i) & 1u) {
-                const uint32_t d = (static_cast<uint32_t>(key[i]) >> shift) & ((1 << bits) - 1);
-                const uint32_t p = lds.base[d] + lds.count[wave][d] + rank[i];
-                if (last) {
-                    s.key[p] = key[i];
-                    s.tok[p] = tok[i];
-                } else {
-                    keys[p] = key[i];
-                    toks[p] = static_cast<uint16_t>(tok[i]);
-                }
+    for (int c = 0; c < kBucketHold; ++c)
+        look(held[c]);
+#pragma unroll 4
+    for (int c = kBucketHold; c < chunks; ++c) {
+        const int t = first + 64 * c;
+        look(t < n ? key_of(a, t) : none);
+    }
+    if (lane == 0) {
+        wave_in[wave] = in;
+        wave_below[wave] = below;
+        wave_rows[wave] = listed;
+    }
+    for (int d = tid; d < bins; d += kBucketThreads)
+#pragma unroll
+        for (int w = 0; w < kBucketWaves; ++w)
+            count[w][d] = 0;
+    __syncthreads();
+    uint32_t start = 0, mine = 0, all = 0, rows = 0;
+#pragma unroll
+    for (int w = 0; w < kBucketWaves; ++w) {
+        start += wave_below[w];
+        mine += w < wave ? wave_in[w] : 0;
+        all += wave_in[w];
+        rows += wave_rows[w];
+    }
+    for (uint32_t p = rows + bucket * kBucketThreads + tid; p < a.n; p += gridDim.x * kBucketThreads)
+        s.key[p] = none;   /* its token is not looked at */
+    if (all == 0)
+        return;
+    /* the bucket's tokens in order of position, to their part of the list */
+    uint32_t at = start + mine;
+    auto collect = [&](int t, int32_t key) {
+        const uint64_t got = __ballot(key < none && (static_cast<uint32_t>(key) & mask) == bucket);
+        if ((got >> lane) & 1u) {
+            const uint32_t p = at + __builtin_popcountll(got & ((uint64_t{1} << lane) - 1));
+            s.key_mid[p] = key;
+            s.tok_mid[p] = t;
+        }
+        at += __builtin_popcountll(got);
+    };
+#pragma unroll
+    for (int c = 0; c < kBucketHold; ++c)
+        collect(first + 64 * c, held[c]);
+#pragma unroll 4
+    for (int c = kBucketHold; c < chunks; ++c) {
+        const int t = first + 64 * c;
+        collect(t, t < n ? key_of(a, t) : none);
+    }
+    __threadfence_block();
+    __syncthreads();
+    /* how many each wavefront has of every row, then where they go */
+    const int parts = (static_cast<int>(all) + 64 * kBucketWaves - 1) / (64 * kBucketWaves);
+    const uint32_t end = start + all;
+    auto each = [&](auto&& fn) {
+        for (int c = 0; c < parts; ++c) {
+            const uint32_t p = start + (wave * parts + c) * 64 + lane;
+            const bool there = p < end;
+            const int32_t key = there ? s.key_mid[p] : -1;
+            uint64_t same = __ballot(there);   /* lanes with this lane's row */
+            for (int d = 0; (bins - 1) >> d != 0; ++d) {
+                const uint64_t set = __ballot((key >> (shift + d)) & 1);
+                same &= (key >> (shift + d)) & 1 ? set : ~set;
             }
-        if (last)
-            break;
-        __syncthreads();
+            if (there)
+                fn(p, key, same);
+        }
+    };
+    volatile uint32_t* own = count[wave];
+    each([&](uint32_t, int32_t key, uint64_t same) {
+        if ((same & ((uint64_t{1} << lane) - 1)) == 0)
+            own[key >> shift] += __builtin_popcountll(same);
+    });
+    __syncthreads();
+    /* exclusive sums over the rows, and over the wavefronts within one */
+    constexpr int kPer = (kBucketBins + kBucketThreads - 1) / kBucketThreads;
+    uint32_t sums[kPer], total = 0;
 #pragma unroll
-        for (int i = 0; i < kOneItems; ++i)
-            if ((valid >> i) & 1u) {
-                key[i] = keys[at0 + 64 * i];
-                tok[i] = toks[at0 + 64 * i];
+    for (int j = 0; j < kPer; ++j) {
+        const int d = tid * kPer + j;
+        sums[j] = 0;
+        if (d < bins)
+#pragma unroll
+            for (int w = 0; w < kBucketWaves; ++w)
+                sums[j] += count[w][d];
+        total += sums[j];
+    }
+    uint32_t incl = total;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const uint32_t o = __shfl_up(incl, d, 64);
+        if (lane >= d)
+            incl += o;
+    }
+    if (lane == 63)
+        wave_in[wave] = incl;
+    __syncthreads();
+    uint32_t before = start + incl - total;
+    for (int w = 0; w < wave; ++w)
+        before += wave_in[w];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        const int d = tid * kPer + j;
+        if (d < bins)
+#pragma unroll
+            for (int w = 0; w < kBucketWaves; ++w) {
+                const uint32_t c = count[w][d];
+                count[w][d] = before;
+                before += c;
             }
     }
+    __syncthreads();
+    each([&](uint32_t p, int32_t key, uint64_t same) {
+        const uint32_t rank = __builtin_popcountll(same & ((uint64_t{1} << lane) - 1)), to = own[key >> shift] + rank;
+        s.key[to] = key;
+        s.tok[to] = s.tok_mid[p];
+        __builtin_amdgcn_wave_barrier();
+        if (rank == 0)
+            own[key >> shift] += __builtin_popcountll(same);
+        __builtin_amdgcn_wave_barrier();
+    });
 }
 
 /* FIRST: the keys come from the ids, else from the first pass. */
@@ -375,47 +478,69 @@ __global__ __launch_bounds__(kRowThreads) void k_grad_slabs(EmbedGradArgs a, Sla
 {
     const int64_t slab = static_cast<int64_t>(blockIdx.x) * (kRowThreads / LANES) + threadIdx.x / LANES;
     const int64_t col = (static_cast<int64_t>(blockIdx.y) * LANES + threadIdx.x % LANES) * 8;
-    if (slab >= s.count || col >= a.cols)
+    if (slab >= s.count)
         return;
-    const int n = a.cols - col > 8 ? 8 : static_cast<int>(a.cols - col);
-    const int64_t p0 = slab * s.length, p1 = p0 + s.length < a.n ? p0 + s.length : a.n;
+    const int n = a.cols - col > 8 ? 8 : static_cast<int>(a.cols - col);   /* <= 0: no columns */
+    const int64_t p0 = slab * s.length;
+    const int len = a.n - p0 < s.length ? static_cast<int>(a.n - p0) : s.length;
     const int32_t none = static_cast<int32_t>(a.rows);
-    int32_t prev = p0 > 0 ? s.key[p0 - 1] : -1;
-    int32_t next = s.key[p0];
-    bool head = prev == next;     /* the current run began in an earlier slab */
+    /* the slab's list: a whole wavefront has it in a register, an entry per lane, and its branches are scalar */
+    int32_t keys = -1, toks = 0;
+    if constexpr (LANES == 64) {
+        const int lane = threadIdx.x & 63, at = lane < len ? lane : len - 1;
+        keys = s.key[p0 + at];
+        toks = s.tok[p0 + at];
+    }
+    const int32_t prev = p0 > 0 ? s.key[p0 - 1] : -1, behind = p0 + len < a.n ? s.key[p0 + len] : -1;
+    auto key_at = [&](int i) {
+        if constexpr (LANES == 64)
+            return i < len ? __builtin_amdgcn_readlane(keys, i) : __builtin_amdgcn_readfirstlane(behind);
+        else
+            return i < len ? s.key[p0 + i] : behind;
+    };
+    auto tok_at = [&](int i) {
+        if constexpr (LANES == 64)
+            return __builtin_amdgcn_readlane(toks, i);
+        else
+            return s.tok[p0 + i];
+    };
+    bool head = prev == key_at(0);     /* the current run began in an earlier slab */
     float sum[8] = {};
-    for (int64_t p = p0; p < p1; p += kFlight) {
+    for (int p = 0; p < len; p += kFlight) {
         int32_t key[kFlight + 1];
-        float y[kFlight][8], g[kFlight][8];
-        key[0] = next;
+        Raw8<YT> y[kFlight];
+        Raw8<GT> g[kFlight];
+#pragma unroll
+        for (int u = 0; u <= kFlight; ++u)
+            key[u] = p + u <= len ? key_at(p + u) : none;
         if (key[0] >= none)
             return;               /* ids without a row: all that is left */
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            const int64_t q = p + u + 1;
-            key[u + 1] = q < a.n ? s.key[q] : -1;
+            /* behind the slab or the rows: the first once more, which costs nothing */
+            const int i = p + u < len && key[u] < none ? p + u : p;
+            y[u] = load_raw8<YT>(a.dy, static_cast<int64_t>(tok_at(i)) * a.dy_rs + col, n);
         }
 #pragma unroll
-        for (int u = 0; u < kFlight; ++u) {
-            const bool in = p + u < p1 && key[u] < none;
-            if (in) {
-                load8<YT>(a.dy, static_cast<int64_t>(s.tok[p + u]) * a.dy_rs + col, n, y[u]);
-                if (key[u] != key[u + 1])
-                    load8<GT>(a.g, static_cast<int64_t>(key[u]) * a.g_rs + col, n, g[u]);
-            }
-        }
+        for (int u = 0; u < kFlight; ++u)
+            if (p + u < len && key[u] < none && key[u] != key[u + 1])
+                g[u] = load_raw8<GT>(a.g, static_cast<int64_t>(key[u]) * a.g_rs + col, n);
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            if (p + u >= p1 || key[u] >= none)
+            if (p + u >= len || key[u] >= none)
                 break;
+            float x[8];
+            unpack8<YT>(y[u], x);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                sum[e] += y[u][e];
+                sum[e] += x[e];
             const bool ends = key[u] != key[u + 1];
-            if (ends && !head)
-                add8<GT>(a, key[u], col, n, g[u], sum);
-            else if (ends || p + u + 1 == p1)
+            if (ends && !head) {
+                unpack8<GT>(g[u], x);
+                add8<GT>(a, key[u], col, n, x, sum);
+            } else if ((ends || p + u + 1 == len) && n > 0) {
                 store8<HPO_PARAM_FP32>(s.part, (2 * slab + (head ? 0 : 1)) * s.width + col, 8, sum);
+            }
             if (ends) {
                 head = false;
 #pragma unroll
@@ -423,53 +548,106 @@ __global__ __launch_bounds__(kRowThreads) void k_grad_slabs(EmbedGradArgs a, Sla
                     sum[e] = 0.0f;
             }
         }
-        next = key[kFlight];
     }
 }
 
-constexpr int kJoinWaves = 4;
+constexpr int kJoinWaves = 8;
+constexpr int kJoinAlone = 8;   /* slabs whose parts one wavefront adds up */
 
-/* The runs that cross borders: the slab in which one begins adds up its parts, in order within
- * each of four interleaved sequences and then these. */
+/* Sum of the runs' first parts of slabs from .. to - 1, every `step`-th, in order. */
+__device__ __forceinline__ void sum_parts(const Slabs& s, int64_t from, int64_t to, int step, int64_t col, bool any, float (&sum)[8])
+{
+    for (int64_t j = from; j < to; j += step * kFlight) {
+        Raw8<HPO_PARAM_FP32> x[kFlight];
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            const int64_t k = j + u * step;
+            x[u] = load_raw8<HPO_PARAM_FP32>(s.part, 2 * (k < to ? k : j) * s.width + col, any && k < to ? 8 : 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            float y[8];
+            unpack8<HPO_PARAM_FP32>(x[u], y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum[e] += y[e];
+        }
+    }
+}
+
+/* The runs that cross borders: a wavefront looks whether one begins in its slab, and adds up the run's parts in
+ * order.  Where these are many, the workgroup's wavefronts take every eighth each, and the sums of the eight
+ * are added in order. */
 template <int GT>
 __global__ __launch_bounds__(64 * kJoinWaves) void k_grad_join(EmbedGradArgs a, Slabs s)
 {
     __shared__ float other[kJoinWaves][64][8];
+    __shared__ int64_t behind[kJoinWaves];   /* of a long run that begins in the wavefront's slab, its end; else 0 */
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int64_t col = (static_cast<int64_t>(blockIdx.y) * 64 + lane) * 8;
     const int n = a.cols - col > 8 ? 8 : static_cast<int>(a.cols - col);   /* <= 0: no columns */
     const int32_t none = static_cast<int32_t>(a.rows);
-    for (int64_t slab = blockIdx.x; slab + 1 < s.count; slab += gridDim.x) {
+    const int64_t slab = static_cast<int64_t>(blockIdx.x) * kJoinWaves + wave;
+    int64_t last = 0;
+    int32_t key = none;
+    if (slab + 1 < s.count) {
         const int64_t p0 = slab * s.length, p1 = p0 + s.length;
-        const int32_t key = s.key[p1 - 1];
-        if (key >= none)
-            return;
-        if (s.key[p1] != key || (s.key[p0] == key && p0 > 0 && s.key[p0 - 1] == key))
-            continue;   /* nothing crosses, or it began earlier */
-        float sum[8] = {};
-        for (int64_t j = slab + 1 + wave; j < s.count && s.key[j * s.length] == key; j += kJoinWaves) {
-            float x[8];
-            load8<HPO_PARAM_FP32>(s.part, 2 * j * s.width + col, n > 0 ? 8 : 0, x);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                sum[e] += x[e];
+        const int32_t next = s.key[p1], first = s.key[p0], prev = s.key[p0 > 0 ? p0 - 1 : 0];
+        key = s.key[p1 - 1];
+        if (key < none && next == key && !(first == key && p0 > 0 && prev == key)) {
+            last = slab + 1;
+            for (;;) {
+                const int64_t j = last + lane;
+                const uint64_t on = __ballot(j < s.count && s.key[(j < s.count ? j : s.count - 1) * s.length] == key);
+                const int more = on == ~uint64_t{0} ? 64 : __builtin_ctzll(~on);
+                last += more;
+                if (more < 64)
+                    break;
+            }
         }
-        __syncthreads();
+    }
+    auto finish = [&](const float (&sum)[8]) {
+        if (n <= 0)
+            return;
+        float x[8], g[8];
+        load8<HPO_PARAM_FP32>(s.part, (2 * slab + 1) * s.width + col, 8, x);
+        load8<GT>(a.g, static_cast<int64_t>(key) * a.g_rs + col, n, g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] += sum[e];
+        add8<GT>(a, key, col, n, g, x);
+    };
+    const bool far = last - slab > kJoinAlone;
+    if (lane == 0)
+        behind[wave] = far ? last : 0;
+    __syncthreads();
+    if (last > 0 && !far) {
+        float sum[8] = {};
+        sum_parts(s, slab + 1, last, 1, col, n > 0, sum);
+        finish(sum);
+    }
+    for (int w = 0; w < kJoinWaves; ++w) {
+        const int64_t end = behind[w];
+        if (end == 0)
+            continue;
+        float sum[8] = {};
+        sum_parts(s, static_cast<int64_t>(blockIdx.x) * kJoinWaves + w + 1 + wave, end, kJoinWaves, col, n > 0, sum);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             other[wave][lane][e] = sum[e];
         __syncthreads();
-        if (wave == 0 && n > 0) {
-            float x[8], g[8];
-            load8<HPO_PARAM_FP32>(s.part, (2 * slab + 1) * s.width + col, 8, x);
-            load8<GT>(a.g, static_cast<int64_t>(key) * a.g_rs + col, n, g);
+        if (wave == w) {
 #pragma unroll
-            for (int w = 0; w < kJoinWaves; ++w)
+            for (int e = 0; e < 8; ++e)
+                sum[e] = 0.0f;
+#pragma unroll
+            for (int v = 0; v < kJoinWaves; ++v)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    x[e] += other[w][lane][e];
-            add8<GT>(a, key, col, n, g, x);
+                    sum[e] += other[v][lane][e];
+            finish(sum);
         }
+        __syncthreads();
     }
 }
 
@@ -558,12 +736,14 @@ hipError_t embedding_out(const EmbedArgs& a, hipStream_t stream)
     return embedding<WT, HPO_PARAM_FP32>(a, stream);
 }
 
-/* Tokens of a slab: 16, more where that still leaves every CU some 64 wavefronts. */
+/* Tokens of a slab: the more the fewer runs cross borders, as long as there are some 6144 wavefronts (6 a
+ * SIMD).  The sums and the join of bf16 rows: 20000 of 1001 take 27 us with slabs of 8 and 34 with 16; 8192 of 4096
+ * 44 and 39. */
 int32_t slab_length(int64_t n, int64_t cols)
 {
     const int64_t pieces = (cols + 511) / 512;
-    int32_t l = 16;
-    while (l < 64 && (n + l - 1) / l * pieces > 16384)
+    int32_t l = 8;
+    while (l < 64 && (n + l - 1) / l * pieces > 6144)
         l *= 2;
     return l;
 }
@@ -576,7 +756,7 @@ int64_t carve(int64_t n, int64_t cols, void* ws, Sorted* s, Slabs* b)
     if (n <= kFewMax)
         return 0;
     const int64_t list = pad256(4 * n), blocks = (n + kBlockTokens - 1) / kBlockTokens;
-    const int64_t mid = n > kOneMax ? 2 * list + pad256(4 * blocks * kBins) : 0;
+    const int64_t mid = 2 * list + (n > kBucketMax ? pad256(4 * blocks * kBins) : 0);
     const int32_t length = slab_length(n, cols);
     const int64_t count = (n + length - 1) / length, width = (cols + 7) / 8 * 8;
     const int64_t part = pad256(8 * count * width);
@@ -601,12 +781,16 @@ int64_t carve(int64_t n, int64_t cols, void* ws, Sorted* s, Slabs* b)
 /* Sorts the tokens by row of the table. */
 hipError_t sort_tokens(const EmbedGradArgs& a, const Sorted& s, hipStream_t stream)
 {
+    if (a.n <= kBucketMax) {
+        int shift = 8;   /* 256 buckets: one workgroup a CU */
+        while (((a.rows - 1) >> shift) + 1 > kBucketBins)
+            ++shift;
+        return launch(k_sort_bucket, dim3(1u << shift), kBucketThreads, stream, a, s, shift);
+    }
     int bits = 1;
     while ((a.rows >> bits) != 0)   /* keys are 0 .. rows */
         ++bits;
     const int bits0 = bits <= kDigitBits ? bits : (bits + 1) / 2, bits1 = bits - bits0;
-    if (a.n <= kOneMax)
-        return launch(k_sort_one, dim3(1), kSortThreads, stream, a, s, bits0, bits1);
     const dim3 grid(static_cast<uint32_t>((a.n + kBlockTokens - 1) / kBlockTokens));
     hipError_t e = launch(k_sort_count<true>, grid, kSortThreads, stream, a, s, 0, bits0);
     if (e != hipSuccess)
@@ -633,7 +817,7 @@ hipError_t embedding_grad(const EmbedGradArgs& a, const Slabs& b, hipStream_t st
                           kRowThreads, stream, a, b);
     if (e != hipSuccess || b.count == 1)
         return e;
-    return launch(k_grad_join<GT>, dim3(static_cast<uint32_t>(std::min<int64_t>(b.count - 1, 1024)),
+    return launch(k_grad_join<GT>, dim3(static_cast<uint32_t>((b.count + kJoinWaves - 2) / kJoinWaves),
                                         static_cast<uint32_t>((a.cols + 511) / 512)),
                   64 * kJoinWaves, stream, a, b);
 }

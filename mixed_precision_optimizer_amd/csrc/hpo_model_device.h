@@ -18,6 +18,7 @@ typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 /* Vectors at any element's address: global memory takes such an access in one
  * instruction, a line more where it straddles one. */
 typedef f32x4_t f32x4_any __attribute__((aligned(4)));
+typedef u32x4_t u32x4_any4 __attribute__((aligned(4)));
 typedef u32x4_t u32x4_any2 __attribute__((aligned(2)));
 typedef u32x2_t u32x2_any2 __attribute__((aligned(2)));
 typedef u32x4_t u32x4_any __attribute__((aligned(1)));
@@ -48,45 +49,65 @@ __device__ __forceinline__ uint32_t narrow(float x)
     return DT == HPO_PARAM_BF16 ? bf16_rne_bits(x) : f16_bits(x);
 }
 
-/* Eight consecutive elements of type DT from element `at` on, n of them in the row (n <= 0: none; the
- * others come as 0). */
+/* Eight consecutive elements of type DT as they are stored: loads that nothing waits for yet. */
 template <int DT>
-__device__ __forceinline__ void load8(const void* base, int64_t at, int n, float (&x)[8])
+struct Raw8 {
+    u32x4_t v[DT == HPO_PARAM_FP32 ? 2 : 1];
+};
+
+/* From element `at` on, n of them in the row (n <= 0: none; the others come as 0). */
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load_raw8(const void* base, int64_t at, int n)
 {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        x[e] = 0.0f;
+    Raw8<DT> r;
     if constexpr (DT == HPO_PARAM_FP32) {
-        const float* p = static_cast<const float*>(base) + at;
+        const uint32_t* p = static_cast<const uint32_t*>(base) + at;
         if (n >= 8) {
-            const f32x4_t lo = *reinterpret_cast<const f32x4_any*>(p), hi = *reinterpret_cast<const f32x4_any*>(p + 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[e] = lo[e];
-                x[4 + e] = hi[e];
-            }
+            r.v[0] = *reinterpret_cast<const u32x4_any4*>(p);
+            r.v[1] = *reinterpret_cast<const u32x4_any4*>(p + 4);
         } else {
+            r.v[0] = u32x4_t{0, 0, 0, 0};
+            r.v[1] = u32x4_t{0, 0, 0, 0};
 #pragma unroll
             for (int e = 0; e < 7; ++e)
                 if (e < n)
-                    x[e] = p[e];
+                    r.v[e >> 2][e & 3] = p[e];
         }
     } else {
         const uint16_t* p = static_cast<const uint16_t*>(base) + at;
         if (n >= 8) {
-            const u32x4_t t = *reinterpret_cast<const u32x4_any2*>(p);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                x[2 * e] = widen<DT>(t[e] & 0xffffu);
-                x[2 * e + 1] = widen<DT>(t[e] >> 16);
-            }
+            r.v[0] = *reinterpret_cast<const u32x4_any2*>(p);
         } else {
+            r.v[0] = u32x4_t{0, 0, 0, 0};
 #pragma unroll
             for (int e = 0; e < 7; ++e)
                 if (e < n)
-                    x[e] = widen<DT>(p[e]);
+                    r.v[0][e >> 1] |= static_cast<uint32_t>(p[e]) << (16 * (e & 1));
         }
     }
+    return r;
+}
+
+template <int DT>
+__device__ __forceinline__ void unpack8(const Raw8<DT>& r, float (&x)[8])
+{
+    if constexpr (DT == HPO_PARAM_FP32) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            x[e] = __uint_as_float(r.v[e >> 2][e & 3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            x[2 * e] = widen<DT>(r.v[0][e] & 0xffffu);
+            x[2 * e + 1] = widen<DT>(r.v[0][e] >> 16);
+        }
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ void load8(const void* base, int64_t at, int n, float (&x)[8])
+{
+    unpack8<DT>(load_raw8<DT>(base, at, n), x);
 }
 
 template <int DT>
