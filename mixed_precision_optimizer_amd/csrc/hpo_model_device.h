@@ -49,6 +49,31 @@ __device__ __forceinline__ uint32_t narrow(float x)
     return DT == HPO_PARAM_BF16 ? bf16_rne_bits(x) : f16_bits(x);
 }
 
+/* Two neighbours of type DT, rounded to nearest even by the hardware's conversion (a NaN stays one). */
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    if constexpr (DT == HPO_PARAM_BF16)
+        return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{a, b}), bf16x2));
+    else
+        return f16_bits(a) | (f16_bits(b) << 16);
+}
+
+/* n of eight 16-bit elements (n <= 0: none) as they are. */
+__device__ __forceinline__ void store_raw8(uint16_t* p, int n, u32x4_t x)
+{
+    if (n >= 8) {
+        *reinterpret_cast<u32x4_any2*>(p) = x;
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 7; ++e)
+        if (e < n)
+            p[e] = static_cast<uint16_t>(x[e >> 1] >> (16 * (e & 1)));
+}
+
 /* Eight consecutive elements of type DT as they are stored: loads that nothing waits for yet. */
 template <int DT>
 struct Raw8 {

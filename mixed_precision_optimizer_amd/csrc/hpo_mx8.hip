@@ -131,7 +131,7 @@ __global__ __launch_bounds__(T::kThreads) void k_mx8_linear(ProductArgs p)
     __shared__ __attribute__((aligned(16))) char lds[4 * kSlice + 2 * kScaleStage];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int frow = lane & 31, fh = lane >> 5;
-    const Work w = work_of(p);
+    const Work w = work_of(p, blockIdx.x, gridDim.x);
     const int64_t m0 = static_cast<int64_t>(w.tm) * T::BM, n0 = static_cast<int64_t>(w.tn) * T::BN;
     const int rows_m = p.m - m0 < T::BM ? static_cast<int>(p.m - m0) : T::BM;
     const int rows_n = p.n - n0 < T::BN ? static_cast<int>(p.n - n0) : T::BN;
@@ -214,22 +214,11 @@ __global__ __launch_bounds__(T::kThreads) void k_mx8_linear(ProductArgs p)
         }
     };
     auto put_scales = [&](int at) {
-        if (late > 0) {
-#pragma unroll
-            for (int c = 0; c < kScaleRows; ++c) {
-                uint64_t lo = sheld[c][0] | (static_cast<uint64_t>(sheld[c][1]) << 32);
-                uint64_t hi = sheld[c][2] | (static_cast<uint64_t>(sheld[c][3]) << 32);
-                lo = late < 64 ? (lo >> late) | (hi << (64 - late)) : hi >> (late - 64);
-                hi = late < 64 ? hi >> late : 0;
-                sheld[c] = u32x4_t{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
-                                   static_cast<uint32_t>(hi >> 32)};
-            }
-        }
 #pragma unroll
         for (int c = 0; c < kScaleRows; ++c) {
             const int r = c * T::kThreads + tid;
             if (kRows % T::kThreads == 0 || r < kRows)
-                *reinterpret_cast<u32x4_t*>(lds + at + r * 16) = sheld[c];
+                *reinterpret_cast<u32x4_t*>(lds + at + r * 16) = drop_bytes(sheld[c], late);
         }
     };
 
@@ -357,6 +346,335 @@ __global__ __launch_bounds__(T::kThreads) void k_mx8_linear(ProductArgs p)
     epilogue<T, false>(p, w, lds, acc);
 }
 
+/* The same on tiles of 256 x 256 by four wavefronts, one a SIMD with half of its registers in sums: a
+ * wavefront's 128 x 128 block reads a third less from LDS for the same products than two of 128 x 64, and the
+ * matrix cores' blocks of 16 x 16 x 128 draw less power than those of 32 x 32 x 64 (random data, operands in
+ * registers: 4.45 and 3.87 PFLOP/s).
+ *
+ * Of a stage of 128 k all fragments of B are in registers, those of A come row block by row block, one group of eight
+ * matrix instructions ahead.  Two stages are in LDS.  B's half of this one is free once its fragments are read (barrier
+ * X, behind group 0), A's before the last group (barrier Y, where the next stage must have landed and its fragments
+ * begin to replace those of this one): what is fetched into them is the stage after next, B in groups 1 to 4, A in
+ * group 7 and the next stage's group 0.  Lane (r, g) = (lane % 16, lane / 16) of a block holds of row r bytes 16 g ..
+ * 16 g + 15 of the first 64 and of the second, and the scale of the g-th 32.
+ *
+ * A workgroup a CU takes tile after tile, and the stages of the next follow those of this one without a gap, so that
+ * its first loads run beside this one's last products and results. */
+struct Big {
+    static constexpr int kThreads = 256, kSide = 256;
+};
+
+/* The wavefront's sums leave, 16 rows at a time; results of 16 bits through LDS, so that whole rows leave in runs of
+ * 256 bytes.  `c` is the block's first element; acc[i][j][r] of a lane: row 16 i + lane % 16, column
+ * 16 j + 4 (lane / 16) + r.  The code is kept short (one path for whole blocks, a loop for others): it runs once a tile, and
+ * what does not stay in the instruction cache costs more than the stores. */
+/* Sums out of the accumulation registers, here and not before: left to itself the compiler moves all 256 of a lane out
+ * at the loop's end, into memory where it has to. */
+__device__ __forceinline__ f32x4_t taken(f32x4_t a)
+{
+    f32x4_t v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float s = a[e];
+        float x;
+        asm volatile("v_accvgpr_read_b32 %0, %1" : "=v"(x) : "a"(s));
+        v[e] = x;
+    }
+    return v;
+}
+
+template <int DT>
+__device__ __forceinline__ void write_big(char* mine, void* c, int64_t rs, int rows, int cols, const f32x4_t (&acc)[8][8])
+{
+    int lane = threadIdx.x & 63;
+    /* Behind an empty asm the addresses below are this tile's: else the compiler forms them before the loop over the
+     * tiles, more of them than there are registers. */
+    asm volatile("" : "+v"(lane), "+s"(rs));
+    const int frow = lane & 15, fg = lane >> 4;
+    const bool whole = rows >= 128 && cols >= 128;
+    /* the last matrix instructions' results, for reads that the compiler does not know to be such: 16 passes */
+    asm volatile("s_nop 15\n\ts_nop 15");
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (DT == HPO_PARAM_FP32) {
+        float* dst = static_cast<float*>(c) + frow * rs + 4 * fg;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (whole) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<f32x4_any*>(dst + 16 * j) = taken(acc[i][j]);
+            } else if (16 * i + frow < rows) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const f32x4_t x = taken(acc[i][j]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (16 * j + 4 * fg + e < cols)
+                            dst[16 * j + e] = x[e];
+                }
+            }
+            dst += 16 * rs;
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    } else {
+        uint16_t* dst = static_cast<uint16_t*>(c) + fg * rs + 8 * frow;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const f32x4_t x = taken(acc[i][j]);
+                *reinterpret_cast<u32x2_t*>(mine + frow * 256 + (((2 * j + (fg >> 1)) ^ frow) << 4) + (fg & 1) * 8) =
+                    u32x2_t{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])};
+            }
+            __builtin_amdgcn_wave_barrier();
+            if (whole) {
+                u32x4_t x[4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    x[t] = *reinterpret_cast<const u32x4_t*>(mine + (4 * t + fg) * 256 + ((frow ^ (4 * t + fg)) << 4));
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+                    *reinterpret_cast<u32x4_any2*>(dst + 4 * t * rs) = x[t];
+            } else {
+#pragma unroll 1
+                for (int t = 0; t < 4; ++t) {
+                    const u32x4_t x = *reinterpret_cast<const u32x4_t*>(mine + (4 * t + fg) * 256 + ((frow ^ (4 * t + fg)) << 4));
+                    if (16 * i + 4 * t + fg < rows)
+                        store_raw8(dst + 4 * t * rs, cols - 8 * frow, x);
+                }
+            }
+            dst += 16 * rs;
+            __builtin_amdgcn_wave_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+}
+
+__global__ __launch_bounds__(Big::kThreads, 1) void k_mx8_linear_big(ProductArgs p, uint32_t items)
+{
+    constexpr int kSide = Big::kSide, kHalf = kSide * kRowBytes, kStage = 2 * kHalf, kScales = 2 * kStage,
+                  kScaleStage = 2 * kSide * 16, kOut = kScales + 2 * kScaleStage;
+    __shared__ __attribute__((aligned(16))) char lds[kOut + 4 * 4096];
+    const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+    const int frow = lane & 15, fg = lane >> 4;
+    const int64_t nb = (p.k + kMxBlock - 1) / kMxBlock;
+    const int steps = static_cast<int>((p.k + 127) / 128);
+    const int ldA = static_cast<int>(p.a_rs), ldB = static_cast<int>(p.b_rs);
+    int voffA[2], voffB[2], piece[2];
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        piece[c] = ((lane & 7) ^ row_swizzle(8 * c + (lane >> 3))) * 16;
+        voffA[c] = (wave * 64 + (lane >> 3)) * ldA + piece[c];
+        voffB[c] = (wave * 64 + (lane >> 3)) * ldB + piece[c];
+    }
+    auto first_of = [&](const Work& w) { return static_cast<int>(static_cast<int64_t>(steps) * w.split / p.splits); };
+    auto end_of = [&](const Work& w) { return static_cast<int>(static_cast<int64_t>(steps) * (w.split + 1) / p.splits); };
+    /* Where an operand's stages come from: the rows of its tile, and which stage is next.  Behind the last item stages
+     * come as zeros from nowhere, so that the loads in flight stay as many. */
+    struct Source {
+        const uint8_t* base;
+        int bytes, kt, end;
+    };
+    auto open = [&](Source& s, bool b, uint32_t item) {
+        s.kt = s.end = steps;
+        s.bytes = 0;
+        s.base = p.b;
+        if (item < items) {
+            const Work w = work_of(p, item, items);
+            const int64_t r0 = static_cast<int64_t>(b ? w.tn : w.tm) * kSide, all = b ? p.n : p.m;
+            const int rows = all - r0 < kSide ? static_cast<int>(all - r0) : kSide;
+            s.base = uniform(b ? p.b + w.z * p.b_bs + r0 * p.b_rs
+                               : static_cast<const uint8_t*>(p.a) + w.z * p.a_bs + r0 * p.a_rs);
+            s.bytes = uniform((rows - 1) * (b ? ldB : ldA) + static_cast<int>(p.k));
+            s.kt = uniform(first_of(w));
+            s.end = uniform(end_of(w));
+        }
+    };
+    Source ca, cb, na, nxb;   /* now, and of the next item */
+    auto advance = [&](Source& s, const Source& next) {
+        if (++s.kt >= s.end)
+            s = next;
+    };
+    /* load i of eight of a half */
+    auto fetch = [&](const Source& s, bool b, int buf, int i) {
+        const int left = static_cast<int>(p.k) - s.kt * kRowBytes;
+        const int v = left >= kRowBytes || piece[i & 1] < left ? (b ? voffB : voffA)[i & 1] : kNowhere;
+        buffer_load_lds16(__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(s.base), 0, s.bytes, 0x00020000),
+                          lds + buf * kStage + (b ? kHalf : 0) + (wave * 8 + i) * 1024, v,
+                          (left > 0 ? s.kt * kRowBytes : 0) + i * 8 * (b ? ldB : ldA));
+    };
+    /* Scales of four stages at a time, a row of A and one of B a lane (see k_mx8_linear) */
+    const uint8_t* srow[2] = {p.a_scales, p.b_scales};
+    u32x4_t sheld[2];
+    int late = 0;
+    auto open_scales = [&](const Work& w) {
+        const int64_t m = static_cast<int64_t>(w.tm) * kSide + tid, n = static_cast<int64_t>(w.tn) * kSide + tid;
+        srow[0] = p.a_scales + (w.z * p.m + (m < p.m ? m : p.m - 1)) * nb;
+        srow[1] = p.b_scales + (w.z * p.n + (n < p.n ? n : p.n - 1)) * nb;
+        const int64_t at = 4 * static_cast<int64_t>(first_of(w));
+        late = 0;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            sheld[c] = load16(srow[c] + at, nb - at);
+    };
+    auto fetch_scales = [&](int64_t at) {
+        if (nb >= 16) {
+            const int64_t start = at < nb - 16 ? at : nb - 16;
+            late = at - start < 16 ? static_cast<int>(at - start) * 8 : 0;
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                sheld[c] = *reinterpret_cast<const u32x4_any*>(srow[c] + start);
+        }
+    };
+    auto put_scales = [&](int buf) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<u32x4_t*>(lds + kScales + buf * kScaleStage + (c * kSide + tid) * 16) = drop_bytes(sheld[c], late);
+    };
+
+    f32x4_t acc[8][8];
+    const int am = wave / 2 * 128 + frow, bn = wave % 2 * 128 + frow;
+    const int base_a = piece_at(am, fg), base_b = kHalf + piece_at(bn, fg);
+    auto frag = [&](int base, int block) {
+        const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(lds + base + block * (16 * kRowBytes));
+        const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(lds + (base ^ 64) + block * (16 * kRowBytes));
+        return i32x8_t{static_cast<int>(lo[0]), static_cast<int>(lo[1]), static_cast<int>(lo[2]), static_cast<int>(lo[3]),
+                       static_cast<int>(hi[0]), static_cast<int>(hi[1]), static_cast<int>(hi[2]), static_cast<int>(hi[3])};
+    };
+    i32x8_t fa[2], fb[8];
+    int sa[8], sb[8];
+    const int scale_a = kScales + am * 16 + fg, scale_b = kScales + (kSide + bn) * 16 + fg;
+    auto scale_at = [&](int base, int block) {
+        return static_cast<int>(*reinterpret_cast<const uint8_t*>(lds + base + block * 256));
+    };
+    auto barrier = [&](auto loads) {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(waitcnt(decltype(loads)::value));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    uint32_t item = blockIdx.x;
+    Work w = work_of(p, item, items);
+    open(ca, false, item);
+    open(cb, true, item);
+    open_scales(w);
+    put_scales(0);
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        fetch(cb, true, 0, c);
+    ++cb.kt;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        fetch(ca, false, 0, c);
+    ++ca.kt;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        fetch(cb, true, 1, c);
+    ++cb.kt;   /* an item has four stages at least */
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        fetch(ca, false, 1, c);
+    barrier(std::integral_constant<int, 12>{});
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        fb[j] = frag(base_b, j);
+    fa[0] = frag(base_a, 0);
+    int buf = 0;
+    for (;;) {
+        const int k0 = uniform(first_of(w)), k1 = uniform(end_of(w));
+        open(na, false, item + gridDim.x);
+        open(nxb, true, item + gridDim.x);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            sb[j] = scale_at(scale_b, j);
+            sa[j] = scale_at(scale_a, j);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                acc[i][j] = f32x4_t{0, 0, 0, 0};
+        for (int kt = k0; kt < k1; ++kt) {
+            const unsigned at = static_cast<unsigned>(kt - k0);
+            const int next_scale = static_cast<int>((at + 1) >> 2 & 1) * kScaleStage + static_cast<int>((at + 1) & 3) * 4;
+            int here_a = base_a + buf * kStage, next_a = base_a + (buf ^ 1) * kStage, next_b = base_b + (buf ^ 1) * kStage;
+            int next_sa = scale_a + next_scale, next_sb = scale_b + next_scale;
+            asm volatile("" : "+v"(here_a), "+v"(next_a), "+v"(next_b), "+v"(next_sa), "+v"(next_sb));
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i < 7) {
+                    fa[(i + 1) & 1] = frag(here_a, i + 1);
+                } else {
+                    barrier(std::integral_constant<int, 8>{});   /* barrier Y: only what groups 1 to 4 fetched may be in flight */
+                    fa[0] = frag(next_a, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[j], fa[i & 1], acc[i][j], 0, 0, 0, sb[j], 0,
+                                                                                 sa[i]);
+                    if (i == 7) {
+                        fb[j] = frag(next_b, j);
+                        sb[j] = scale_at(next_sb, j);
+                        if (j & 1)
+                            fetch(ca, false, buf, j >> 1);
+                    } else if (i == 0) {
+                        if (j & 1)
+                            fetch(ca, false, buf ^ 1, 4 + (j >> 1));
+                    } else if (i < 5) {
+                        if ((j & 3) == 3)
+                            fetch(cb, true, buf, 2 * (i - 1) + (j >> 2));
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                sa[i] = scale_at(next_sa, i);
+                if (i == 0) {
+                    __builtin_amdgcn_s_barrier();   /* barrier X: every wavefront has its fragments of B */
+                    __builtin_amdgcn_sched_barrier(0);
+                    advance(ca, na);
+                }
+                if (i == 5) {
+                    advance(cb, nxb);
+                    /* four stages' scales are fetched in the second of the four before and put down in the third */
+                    if ((at & 3) == 1)
+                        fetch_scales(4 * static_cast<int64_t>(kt + 3));
+                    if ((at & 3) == 2)
+                        put_scales(static_cast<int>(at >> 2 & 1) ^ 1);
+                }
+            }
+            buf ^= 1;
+        }
+        const Work done = w;
+        item += gridDim.x;
+        if (item < items) {
+            w = work_of(p, item, items);
+            open_scales(w);
+        }
+        const int64_t r0 = static_cast<int64_t>(done.tm) * kSide + wave / 2 * 128;
+        const int64_t c0 = static_cast<int64_t>(done.tn) * kSide + wave % 2 * 128;
+        const int rows = p.m - r0 < 128 ? static_cast<int>(p.m - r0) : 128, cols = p.n - c0 < 128 ? static_cast<int>(p.n - c0) : 128;
+        char* mine = lds + kOut + wave * 4096;
+        if (rows > 0 && cols > 0) {
+            if (p.splits > 1)
+                write_big<HPO_PARAM_FP32>(mine, p.part + ((done.z * p.splits + done.split) * p.m + r0) * p.n + c0, p.n, rows, cols,
+                                          acc);
+            else if (p.c_dtype == HPO_PARAM_BF16)
+                write_big<HPO_PARAM_BF16>(mine, static_cast<uint16_t*>(p.c) + done.z * p.c_bs + r0 * p.c_rs + c0, p.c_rs, rows,
+                                          cols, acc);
+            else
+                write_big<HPO_PARAM_FP16>(mine, static_cast<uint16_t*>(p.c) + done.z * p.c_bs + r0 * p.c_rs + c0, p.c_rs, rows,
+                                          cols, acc);
+        }
+        if (item >= items)
+            break;
+        /* nobody reads scales between the last barrier Y and this one */
+        put_scales(0);
+        barrier(std::integral_constant<int, 63>{});
+    }
+    __builtin_amdgcn_s_waitcnt(waitcnt(0));   /* the zeros, before another workgroup has this LDS */
+}
+
 /* ---------------------------------------------------------------------- */
 /* launches                                                                */
 /* ---------------------------------------------------------------------- */
@@ -459,7 +777,7 @@ hipError_t launch_product(ProductKind kind, ProductArgs p, hipStream_t stream)
     p.splits = c.splits;
     const uint32_t g = static_cast<uint32_t>(grid);
     hipError_t e = kind != kLinear ? launch_mx8_grad(kind == kWgrad, p, c.tile, direct, g, stream)
-                   : c.tile == 256 ? launch(k_mx8_linear<Tile256, true>, dim3(g), Tile256::kThreads, stream, p)
+                   : c.tile == 256 ? launch(k_mx8_linear_big, dim3(std::min<uint32_t>(g, 256)), Big::kThreads, stream, p, g)
                    : c.tile == 128 ? linear_tile<Tile128>(p, direct, g, stream)
                                    : linear_tile<Tile64>(p, direct, g, stream);
     if (e != hipSuccess || p.splits == 1)

@@ -62,7 +62,7 @@ __global__ __launch_bounds__(T::kThreads) void k_mx8_grad(ProductArgs p)
     __shared__ __attribute__((aligned(16))) char lds[2 * kStage];
     const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
     const int frow = lane & 31, fh = lane >> 5;
-    const Work w = work_of(p);
+    const Work w = work_of(p, blockIdx.x, gridDim.x);
     const int64_t m0 = static_cast<int64_t>(w.tm) * T::BM, n0 = static_cast<int64_t>(w.tn) * T::BN;
     const int rows_m = p.m - m0 < T::BM ? static_cast<int>(p.m - m0) : T::BM;
     const int rows_n = p.n - n0 < T::BN ? static_cast<int>(p.n - n0) : T::BN;

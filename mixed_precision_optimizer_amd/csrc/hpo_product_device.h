@@ -38,13 +38,13 @@ using Tile64 = Tile<2, 2, 1, 1>;
 
 constexpr int kRowBytes = 128;   /* of an operand row in a stage: 128 8-bit elements, or 64 16-bit ones */
 constexpr int kStepK = 64;        /* 16-bit elements of k in a stage */
-constexpr int kGroup = 8;        /* tile rows that neighbouring workgroups share */
+constexpr uint32_t kGroup = 8;        /* tile rows that neighbouring workgroups share */
 
 /* Workgroups go to the 8 XCDs round-robin: each XCD gets one contiguous run of the work. */
-__device__ __forceinline__ int64_t xcd_run(int64_t b, int64_t n)
+__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n)
 {
-    constexpr int64_t kXcd = 8;
-    const int64_t x = b % kXcd, k = b / kXcd, q = n / kXcd, r = n % kXcd;
+    constexpr uint32_t kXcd = 8;
+    const uint32_t x = b % kXcd, k = b / kXcd, q = n / kXcd, r = n % kXcd;
     return (x < r ? x * (q + 1) : r * (q + 1) + (x - r) * q) + k;
 }
 
@@ -53,19 +53,30 @@ struct Work {
     int tm, tn, split;
 };
 
-__device__ __forceinline__ Work work_of(const ProductArgs& p)
+/* Item b of n (at most INT32_MAX): the b-th workgroup's, or what a workgroup in its place takes. */
+__device__ __forceinline__ Work work_of(const ProductArgs& p, uint32_t b, uint32_t n)
 {
     Work w;
-    int64_t t = xcd_run(blockIdx.x, gridDim.x);
+    uint32_t t = xcd_run(b, n);
     w.split = static_cast<int>(t % p.splits);
     t /= p.splits;
-    const int64_t per = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+    const uint32_t tiles_n = p.tiles_n, per = p.tiles_m * tiles_n;
     w.z = t / per;
-    const int i = static_cast<int>(t % per), g = i / (kGroup * p.tiles_n), first = g * kGroup;
-    const int rows = p.tiles_m - first < kGroup ? p.tiles_m - first : kGroup, j = i - first * p.tiles_n;
-    w.tm = first + j % rows;
-    w.tn = j / rows;
+    const uint32_t i = t % per, first = i / (kGroup * tiles_n) * kGroup, left = p.tiles_m - first;
+    const uint32_t rows = left < kGroup ? left : kGroup, j = i - first * tiles_n;
+    w.tm = static_cast<int>(first + j % rows);
+    w.tn = static_cast<int>(j / rows);
     return w;
+}
+
+/* The same in every lane: kept in scalar registers. */
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p)
+{
+    const uint64_t a = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32));
+    return reinterpret_cast<const uint8_t*>(lo | static_cast<uint64_t>(hi) << 32);
 }
 
 /* 64 x 16 bytes from a buffer straight into LDS: lane l's lands at dst + 16 l; what lies behind the
@@ -108,6 +119,18 @@ __device__ __forceinline__ u32x4_t load16(const uint8_t* at, int64_t left)
     for (int e = 0; e < left; ++e)
         v[e >> 2] |= static_cast<uint32_t>(at[e]) << (8 * (e & 3));
     return v;
+}
+
+/* v without its first `bits` bits (whole bytes, the same for all lanes); 0 comes in behind. */
+__device__ __forceinline__ u32x4_t drop_bytes(u32x4_t v, int bits)
+{
+    if (bits == 0)
+        return v;
+    uint64_t lo = v[0] | (static_cast<uint64_t>(v[1]) << 32), hi = v[2] | (static_cast<uint64_t>(v[3]) << 32);
+    lo = bits < 64 ? (lo >> bits) | (hi << (64 - bits)) : hi >> (bits - 64);
+    hi = bits < 64 ? hi >> bits : 0;
+    return u32x4_t{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
+                   static_cast<uint32_t>(hi >> 32)};
 }
 
 /* s_waitcnt's operand (gfx9 encoding): at most `loads` in flight, no LDS access. */
