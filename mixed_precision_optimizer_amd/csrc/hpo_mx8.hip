@@ -491,9 +491,13 @@ __global__ __launch_bounds__(Big::kThreads, 1) void k_mx8_linear_big(ProductArgs
         }
     };
     Source ca, cb, na, nxb;   /* now, and of the next item */
+    /* no branch: matrix instructions would sink below it, away from the loads they hide */
     auto advance = [&](Source& s, const Source& next) {
-        if (++s.kt >= s.end)
-            s = next;
+        const bool over = s.kt + 1 >= s.end;
+        s.base = over ? next.base : s.base;
+        s.bytes = over ? next.bytes : s.bytes;
+        s.kt = over ? next.kt : s.kt + 1;
+        s.end = over ? next.end : s.end;
     };
     /* load i of eight of a half */
     auto fetch = [&](const Source& s, bool b, int buf, int i) {
@@ -597,6 +601,11 @@ __global__ __launch_bounds__(Big::kThreads, 1) void k_mx8_linear_big(ProductArgs
                 acc[i][j] = f32x4_t{0, 0, 0, 0};
         for (int kt = k0; kt < k1; ++kt) {
             const unsigned at = static_cast<unsigned>(kt - k0);
+            /* four stages' scales are fetched in the first of the four before and put down in the third */
+            if ((at & 3) == 0)
+                fetch_scales(4 * static_cast<int64_t>(kt + 4));
+            if ((at & 3) == 2)
+                put_scales(static_cast<int>(at >> 2 & 1) ^ 1);
             const int next_scale = static_cast<int>((at + 1) >> 2 & 1) * kScaleStage + static_cast<int>((at + 1) & 3) * 4;
             int here_a = base_a + buf * kStage, next_a = base_a + (buf ^ 1) * kStage, next_b = base_b + (buf ^ 1) * kStage;
             int next_sa = scale_a + next_scale, next_sb = scale_b + next_scale;
@@ -636,11 +645,6 @@ __global__ __launch_bounds__(Big::kThreads, 1) void k_mx8_linear_big(ProductArgs
                 }
                 if (i == 5) {
                     advance(cb, nxb);
-                    /* four stages' scales are fetched in the second of the four before and put down in the third */
-                    if ((at & 3) == 1)
-                        fetch_scales(4 * static_cast<int64_t>(kt + 3));
-                    if ((at & 3) == 2)
-                        put_scales(static_cast<int>(at >> 2 & 1) ^ 1);
                 }
             }
             buf ^= 1;
