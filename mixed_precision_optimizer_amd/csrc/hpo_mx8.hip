@@ -29,7 +29,6 @@ __global__ __launch_bounds__(kSaveThreads) void k_mx8_save(SaveArgs a)
     const int64_t nb = (a.cols + kMxBlock - 1) / kMxBlock, src = z * a.x.bs + i * a.x.rs;
     uint8_t* q = static_cast<uint8_t*>(a.q.data) + z * a.q.bs + i * a.q.rs;
     uint8_t* sc = a.scales + (z * a.rows + i) * nb;
-#pragma unroll 2
     for (int64_t c0 = 0; c0 < a.cols; c0 += 8 * LANES) {   /* all lanes of a block take part to the end */
         const int64_t c = c0 + 8 * (threadIdx.x % LANES);
         const int n = a.cols - c > 8 ? 8 : static_cast<int>(a.cols - c);
@@ -174,7 +173,7 @@ __global__ __launch_bounds__(T::kThreads) void k_mx8_linear(ProductArgs p)
             for (int c = 0; c < kPieces; ++c) {
                 const int i = c * T::kThreads + tid, r = i >> 2, at = (i & 3) * 16;
                 const uint8_t* row = r < T::BM ? A + clamp(r) * p.a_rs : B + clamp(r) * p.b_rs;
-                held[c] = load16(row + k + at, left - at);
+                held[c] = load16(row + k + at, left - at, k + at);
             }
         }
     };
@@ -260,7 +259,7 @@ __global__ __launch_bounds__(T::kThreads) void k_mx8_linear(ProductArgs p)
     if (k0 < k1) {
 #pragma unroll
         for (int c = 0; c < kScaleRows; ++c)
-            sheld[c] = load16(srow[c] + 4 * static_cast<int64_t>(k0), nb - 4 * static_cast<int64_t>(k0));
+            sheld[c] = load16(srow[c] + 4 * static_cast<int64_t>(k0), nb - 4 * static_cast<int64_t>(k0), 0);
         if constexpr (DIRECT) {
 #pragma unroll
             for (int x = 0; x < 3; ++x)
@@ -519,7 +518,7 @@ __global__ __launch_bounds__(Big::kThreads, 1) void k_mx8_linear_big(ProductArgs
         late = 0;
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-            sheld[c] = load16(srow[c] + at, nb - at);
+            sheld[c] = load16(srow[c] + at, nb - at, 0);
     };
     auto fetch_scales = [&](int64_t at) {
         if (nb >= 16) {
@@ -707,22 +706,46 @@ struct Cut {
     int splits;
 };
 
+/* The side of the tiles and the parts of the sum over k (joined afterwards), from an estimate of each choice's time.  A
+ * stage of a workgroup takes `alone` microseconds while it is the only one of its CU, and `shared` for each where
+ * several overlap (two of side 128 and four of side 64 fit), and a join writes and reads every part once.  Small
+ * tiles pay by the bytes they read for each product, large ones by CUs that have nothing to do, parts by the
+ * join.  Both sides measured, in microseconds: hpo_mx8_dgrad of 1024 x 1024 x 65536, side 256 in 16 parts 133, in 8
+ * parts 197, side 128 in 8 parts 151, side 64 in 4 parts 244; of 8 x 256 x 1024 x 1024, side 64 12.9, 128 17.2, 256
+ * 30.5; hpo_mx8_linear of 4096 x 4096 x 1024, side 256 24.3, 128 29.1, 64 39.0; of 512 x 512 x 8192, side 64 in
+ * 4 parts 13.3, whole 23.8, side 128 in 8 parts 16.8.  Over 19 shapes a kind the choice lies 1 to 6 % behind the best.
+ * It depends on the sizes alone, so that the workspace does. */
 Cut cut_of(ProductKind kind, int64_t batch, int64_t m, int64_t n, int64_t k)
 {
-    constexpr int64_t kCus = 256;
-    Cut c{};
+    struct Rate {
+        int tile, fit;
+        double alone, shared;
+    };
+    static constexpr Rate kLinearRates[] = {{256, 1, 1.6, 1.6}, {128, 2, 0.6, 0.55}, {64, 4, 0.3, 0.22}};
+    static constexpr Rate kGradRates[] = {{256, 1, 1.45, 1.45}, {128, 2, 0.7, 0.5}, {64, 4, 0.41, 0.23}};
+    constexpr double kJoin = 2.5, kPartBytes = 6e6;   /* a launch; bytes a microsecond */
     const int64_t depth = kind == kLinear ? 128 : kStepK, steps = (k + depth - 1) / depth;
-    for (int t : {256, 128, 64}) {
-        c.tile = t;
-        c.tiles_m = (m + t - 1) / t;
-        c.tiles_n = (n + t - 1) / t;
-        if (batch * c.tiles_m * c.tiles_n >= kCus / (t == 64 ? 1 : 2))
-            break;
+    const double outputs = static_cast<double>(batch) * static_cast<double>(m) * static_cast<double>(n);
+    Cut best{};
+    double least = 0;
+    for (const Rate& r : kind == kLinear ? kLinearRates : kGradRates) {
+        const int64_t tiles_m = (m + r.tile - 1) / r.tile, tiles_n = (n + r.tile - 1) / r.tile;
+        const int64_t tiles = batch * tiles_m * tiles_n;
+        for (int splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64}) {
+            if (splits > 1 && steps < 2 * splits)
+                break;
+            const int64_t load = (tiles * splits + 255) / 256, rounds = load / r.fit, rest = load % r.fit;   /* of a CU */
+            double us = rounds * std::max(r.alone, r.shared * r.fit) + (rest ? std::max(r.alone, r.shared * rest) : 0);
+            us *= static_cast<double>((steps + splits - 1) / splits + 1);
+            if (splits > 1)
+                us += kJoin + 8 * splits * outputs / kPartBytes;
+            if (best.tile == 0 || us < least) {
+                best = {r.tile, tiles_m, tiles_n, splits};
+                least = us;
+            }
+        }
     }
-    const int64_t tiles = batch * c.tiles_m * c.tiles_n;
-    const int64_t want = tiles >= kCus ? 1 : (2 * kCus + tiles - 1) / tiles, most = std::max<int64_t>(1, steps / 8);
-    c.splits = static_cast<int>(std::min<int64_t>({want, most, 64}));
-    return c;
+    return best;
 }
 
 template <typename T>
@@ -742,9 +765,18 @@ bool is_direct(ProductKind kind, const ProductArgs& p, int tile)
     if (kind == kLinear)
         return p.k % 16 == 0 && on16(p.a, p.a_rs) && on16(p.a, p.a_bs) && on16(p.b, p.b_rs) && on16(p.b, p.b_bs) &&
                tile * p.a_rs + p.k < kReach && tile * p.b_rs + p.k < kReach;
+    if (!on16(p.b, p.b_rs) || !on16(p.b, p.b_bs) || kStepK * p.b_rs + p.n >= kReach)
+        return false;
     if (kind == kDgrad)
         return p.k % 8 == 0 && on16(p.a, 2 * p.a_rs) && on16(p.a, 2 * p.a_bs) && 2 * (tile * p.a_rs + p.k) < kReach;
     return on16(p.a, 2 * p.a_rs) && on16(p.a, 2 * p.a_bs) && 2 * (kStepK * p.a_rs + p.m) < kReach;
+}
+
+/* Whether tiles of 256 can do it: operands that go straight into LDS (beside the sums there are no registers for them),
+ * and for hpo_mx8_linear four stages at least for every workgroup. */
+bool is_big(ProductKind kind, const ProductArgs& p, int splits)
+{
+    return is_direct(kind, p, 256) && (kind != kLinear || (p.k + 127) / 128 >= 4 * splits);
 }
 
 }  // namespace
@@ -767,12 +799,12 @@ int64_t product_workspace(ProductKind kind, int64_t batch, int64_t m, int64_t n,
 hipError_t launch_product(ProductKind kind, ProductArgs p, hipStream_t stream)
 {
     Cut c = cut_of(kind, p.batch, p.m, p.n, p.k);
-    const bool direct = is_direct(kind, p, c.tile);
-    if (!direct && c.tile == 256) {   /* the stages pass through registers, and beside 128 sums there are none */
+    if (c.tile == 256 && !is_big(kind, p, c.splits)) {
         c.tile = 128;
         c.tiles_m = (p.m + 127) / 128;
         c.tiles_n = (p.n + 127) / 128;
     }
+    const bool direct = is_direct(kind, p, c.tile);
     const int64_t grid = p.batch * c.tiles_m * c.tiles_n * c.splits;
     if (grid > INT32_MAX)
         return hipErrorInvalidConfiguration;

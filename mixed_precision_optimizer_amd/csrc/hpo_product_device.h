@@ -58,10 +58,9 @@ __device__ __forceinline__ Work work_of(const ProductArgs& p, uint32_t b, uint32
 {
     Work w;
     uint32_t t = xcd_run(b, n);
-    w.split = static_cast<int>(t % p.splits);
-    t /= p.splits;
-    const uint32_t tiles_n = p.tiles_n, per = p.tiles_m * tiles_n;
-    w.z = t / per;
+    const uint32_t tiles_n = p.tiles_n, per = p.tiles_m * tiles_n, part = t / per;
+    w.z = part / p.splits;
+    w.split = static_cast<int>(part % p.splits);
     const uint32_t i = t % per, first = i / (kGroup * tiles_n) * kGroup, left = p.tiles_m - first;
     const uint32_t rows = left < kGroup ? left : kGroup, j = i - first * tiles_n;
     w.tm = static_cast<int>(first + j % rows);
@@ -110,18 +109,7 @@ __device__ __forceinline__ int pair_swizzle(int k)
         return (k & 2) ^ ((k >> 3) & 1);
 }
 
-/* 16 bytes of a row from `at` on, `left` of them (<= 0: none) inside it; 0 behind. */
-__device__ __forceinline__ u32x4_t load16(const uint8_t* at, int64_t left)
-{
-    u32x4_t v = {0, 0, 0, 0};
-    if (left >= 16)
-        return *reinterpret_cast<const u32x4_any*>(at);
-    for (int e = 0; e < left; ++e)
-        v[e >> 2] |= static_cast<uint32_t>(at[e]) << (8 * (e & 3));
-    return v;
-}
-
-/* v without its first `bits` bits (whole bytes, the same for all lanes); 0 comes in behind. */
+/* v without its first `bits` bits (whole bytes, less than 16 of them); 0 comes in behind. */
 __device__ __forceinline__ u32x4_t drop_bytes(u32x4_t v, int bits)
 {
     if (bits == 0)
@@ -131,6 +119,20 @@ __device__ __forceinline__ u32x4_t drop_bytes(u32x4_t v, int bits)
     hi = bits < 64 ? hi >> bits : 0;
     return u32x4_t{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi),
                    static_cast<uint32_t>(hi >> 32)};
+}
+
+/* 16 bytes of a row from `at` on, `left` of them (<= 0: none) inside it; 0 behind.  `before` bytes of the row lie before
+ * `at`: a row's end is read as the 16 bytes that end there, in one load. */
+__device__ __forceinline__ u32x4_t load16(const uint8_t* at, int64_t left, int64_t before)
+{
+    u32x4_t v = {0, 0, 0, 0};
+    if (left > 0 && (left >= 16 || before + left >= 16)) {
+        const int back = left < 16 ? 16 - static_cast<int>(left) : 0;
+        return drop_bytes(*reinterpret_cast<const u32x4_any*>(at - back), 8 * back);
+    }
+    for (int e = 0; e < left; ++e)
+        v[e >> 2] |= static_cast<uint32_t>(at[e]) << (8 * (e & 3));
+    return v;
 }
 
 /* s_waitcnt's operand (gfx9 encoding): at most `loads` in flight, no LDS access. */
@@ -162,8 +164,7 @@ __device__ __forceinline__ void store4(void* c, int64_t at, int n, f32x4_t x)
     } else {
         uint16_t* p = static_cast<uint16_t*>(c) + at;
         if (n >= 4) {
-            *reinterpret_cast<u32x2_any2*>(p) = u32x2_t{narrow<DT>(x[0]) | (narrow<DT>(x[1]) << 16),
-                                                        narrow<DT>(x[2]) | (narrow<DT>(x[3]) << 16)};
+            *reinterpret_cast<u32x2_any2*>(p) = u32x2_t{pack2<DT>(x[0], x[1]), pack2<DT>(x[2], x[3])};
         } else {
 #pragma unroll
             for (int e = 0; e < 3; ++e)
