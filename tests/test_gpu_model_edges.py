@@ -8,7 +8,7 @@ torch = pytest.importorskip("torch")
 
 import model_util as mu  # noqa: E402
 import stack_util as su  # noqa: E402
-from test_gpu_model import BF16, DEV, E4M3, F16, F32, M, encode, gen, operand, workspace  # noqa: E402,F401
+from test_gpu_model import BF16, DEV, E4M3, F16, F32, M, dgrad, encode, gen, linear, operand, wgrad, workspace  # noqa: E402,F401
 
 pytestmark = pytest.mark.gpu
 
@@ -286,6 +286,24 @@ def test_nan_and_infinity_stay_where_they_enter(M, t, c, r):
     bad[:, (c - 1) // 32 * 32:] = True
     bad[:, :32] = True
     assert torch.equal(~G.isfinite().cpu(), bad)
+
+
+# --------------------------------------------------------------------------
+# large tiles with ragged edges, and sums in parts of unequal lengths
+# --------------------------------------------------------------------------
+@pytest.mark.parametrize("b,t,c,r", [(1, 1000, 40000, 912), (1, 1040, 1008, 30000), (1, 12000, 1040, 1000), (2, 500, 6000, 1000)])
+@pytest.mark.parametrize("layout", ["dense", "aligned"])
+def test_products_in_parts(M, b, t, c, r, layout):
+    linear(M, b, t, c, r, BF16, layout, dev=DEV)
+    dgrad(M, b, t, c, r, F16, BF16, layout, dev=DEV)
+    dgrad(M, b, t, c, r, BF16, F32, layout, dev=DEV)
+    wgrad(M, b, t, c, r, BF16, BF16, layout, True, dev=DEV)
+    wgrad(M, b, t, c, r, F16, F32, layout, False, dev=DEV)
+
+
+@pytest.mark.parametrize("layout", ["dense", "aligned", "padded"])
+def test_linear_in_parts_of_large_tiles(M, layout):
+    linear(M, 1, 1010, 50000, 1000, BF16, layout, dev=DEV)
 
 
 # --------------------------------------------------------------------------
