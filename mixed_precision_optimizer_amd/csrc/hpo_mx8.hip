@@ -363,6 +363,10 @@ struct Big {
     static constexpr int kThreads = 256, kSide = 256;
 };
 
+/* The pieces' order in an LDS row: a fragment read serves rows of two neighbouring pieces at a time, and these 16 lie
+ * in distinct banks (with row_swizzle half of them meet: 2 % of the kernel's time). */
+__device__ __forceinline__ int big_swizzle(int r) { return (r >> 1) & 7; }
+
 /* The wavefront's sums leave, 16 rows at a time; results of 16 bits through LDS, so that whole rows leave in runs of
  * 256 bytes.  `c` is the block's first element; acc[i][j][r] of a lane: row 16 i + lane % 16, column
  * 16 j + 4 (lane / 16) + r.  The code is kept short (one path for whole blocks, a loop for others): it runs once a tile, and
@@ -462,7 +466,7 @@ __global__ __launch_bounds__(Big::kThreads, 1) void k_mx8_linear_big(ProductArgs
     int voffA[2], voffB[2], piece[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        piece[c] = ((lane & 7) ^ row_swizzle(8 * c + (lane >> 3))) * 16;
+        piece[c] = ((lane & 7) ^ big_swizzle(8 * c + (lane >> 3))) * 16;
         voffA[c] = (wave * 64 + (lane >> 3)) * ldA + piece[c];
         voffB[c] = (wave * 64 + (lane >> 3)) * ldB + piece[c];
     }
@@ -537,7 +541,7 @@ __global__ __launch_bounds__(Big::kThreads, 1) void k_mx8_linear_big(ProductArgs
 
     f32x4_t acc[8][8];
     const int am = wave / 2 * 128 + frow, bn = wave % 2 * 128 + frow;
-    const int base_a = piece_at(am, fg), base_b = kHalf + piece_at(bn, fg);
+    const int at = (fg ^ big_swizzle(frow)) << 4, base_a = am * kRowBytes + at, base_b = kHalf + bn * kRowBytes + at;
     auto frag = [&](int base, int block) {
         const u32x4_t lo = *reinterpret_cast<const u32x4_t*>(lds + base + block * (16 * kRowBytes));
         const u32x4_t hi = *reinterpret_cast<const u32x4_t*>(lds + (base ^ 64) + block * (16 * kRowBytes));
