@@ -1,7 +1,8 @@
 /*
  * hpo_mx8.hip -- gfx950 kernels of activations and weights in 8 bits with block
- * scales: the quantisation (hpo_mx8_save) and the products of a linear layer,
- * Y = X^ W^T, dX = dY W^, G += scale * dY^T X^ (hpo_mx8_linear, _dgrad, _wgrad).
+ * scales: the quantisation (hpo_mx8_save), the forward product Y = X^ W^T
+ * (hpo_mx8_linear), the join of sums in parts, and how the products of a linear
+ * layer are cut and launched (the gradients' kernels: hpo_mx8_grad.hip).
  */
 #include <hip/hip_runtime.h>
 
@@ -13,13 +14,15 @@
 namespace hpo {
 namespace {
 
-
 /* ---------------------------------------------------------------------- */
 /* hpo_mx8_save                                                            */
 /* ---------------------------------------------------------------------- */
 constexpr int kSaveThreads = 256;
 
-/* LANES lanes take a row, eight elements each a step; four neighbours hold a scale block. */
+/* byte = the exponent that brings a block's largest magnitude under 448, q = x * 2^(127 - byte) in e4m3.
+ * LANES lanes take a row, eight elements each a step (16 bytes in, 8 out); four neighbours hold a scale block, so its
+ * largest magnitude takes two exchanges and the block is read once.  Bound by HBM: 8192 x 14336 bf16 takes 68 us, 5.2 TB/s
+ * read and written. */
 template <int XT, int LANES>
 __global__ __launch_bounds__(kSaveThreads) void k_mx8_save(SaveArgs a)
 {
@@ -358,7 +361,10 @@ __global__ __launch_bounds__(T::kThreads) void k_mx8_linear(ProductArgs p)
  * 16 g + 15 of the first 64 and of the second, and the scale of the g-th 32.
  *
  * A workgroup a CU takes tile after tile, and the stages of the next follow those of this one without a gap, so that
- * its first loads run beside this one's last products and results. */
+ * its first loads run beside this one's last products and results.
+ *
+ * 8192 x 4096 x 14336: 408 us, 2.36 PFLOP/s (side 128: 644 us); the matrix cores are busy half of the time at the
+ * 2.0 GHz that the power leaves, and wavefronts wait for a fifth of it. */
 struct Big {
     static constexpr int kThreads = 256, kSide = 256;
 };
@@ -367,10 +373,6 @@ struct Big {
  * in distinct banks (with row_swizzle half of them meet: 2 % of the kernel's time). */
 __device__ __forceinline__ int big_swizzle(int r) { return (r >> 1) & 7; }
 
-/* The wavefront's sums leave, 16 rows at a time; results of 16 bits through LDS, so that whole rows leave in runs of
- * 256 bytes.  `c` is the block's first element; acc[i][j][r] of a lane: row 16 i + lane % 16, column
- * 16 j + 4 (lane / 16) + r.  The code is kept short (one path for whole blocks, a loop for others): it runs once a tile, and
- * what does not stay in the instruction cache costs more than the stores. */
 /* Sums out of the accumulation registers, here and not before: left to itself the compiler moves all 256 of a lane out
  * at the loop's end, into memory where it has to. */
 __device__ __forceinline__ f32x4_t taken(f32x4_t a)
@@ -386,6 +388,10 @@ __device__ __forceinline__ f32x4_t taken(f32x4_t a)
     return v;
 }
 
+/* The wavefront's sums leave, 16 rows at a time; results of 16 bits through LDS, so that whole rows leave in runs of
+ * 256 bytes.  `c` is the block's first element; acc[i][j][r] of a lane: row 16 i + lane % 16, column
+ * 16 j + 4 (lane / 16) + r.  The code is kept short (one path for whole blocks, a loop for others): it runs once a tile, and
+ * what does not stay in the instruction cache costs more than the stores. */
 template <int DT>
 __device__ __forceinline__ void write_big(char* mine, void* c, int64_t rs, int rows, int cols, const f32x4_t (&acc)[8][8])
 {

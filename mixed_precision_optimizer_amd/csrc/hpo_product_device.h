@@ -32,7 +32,7 @@ struct Tile {
     static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
     static constexpr int BM = WM * TM * 32, BN = WN * TN * 32;
 };
-using Tile256 = Tile<2, 4, 4, 2>;
+using Tile256 = Tile<2, 4, 4, 2>;   /* of the gradients; hpo_mx8_linear's is Big */
 using Tile128 = Tile<2, 2, 2, 2>;
 using Tile64 = Tile<2, 2, 1, 1>;
 

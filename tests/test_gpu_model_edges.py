@@ -288,6 +288,26 @@ def test_nan_and_infinity_stay_where_they_enter(M, t, c, r):
     assert torch.equal(~G.isfinite().cpu(), bad)
 
 
+@pytest.mark.parametrize("n", [100, 5000, 70000])
+def test_rows_of_padding_are_not_read(M, n):
+    """dY is NaN and infinite where an id has no row: no gradient sees it.  A table without rows gives zeros."""
+    g = gen(n)
+    rows, cols = 37, 40
+    ids = torch.randint(-30, rows + 30, (n,), generator=g)
+    out = (ids < 0) | (ids >= rows)
+    assert 0 < int(out.sum()) < n
+    dy = torch.randn(n, cols, generator=g)
+    dy[out] = torch.where(torch.rand(int(out.sum()), 1, generator=g) < 0.5, math.nan, math.inf)
+    grad = torch.randn(rows, cols, generator=g)
+    G = grad.to(DEV)
+    M.hpo_embedding_grad(ids.to(DEV), dy.to(DEV), G, workspace(M.hpo_embedding_grad_workspace(ids, grad)))
+    want, tol, _ = mu.embedding_grad(ids[~out], dy[~out], grad, 1.0, 0)
+    mu.check(G, want, tol, f"{n}")
+    none = torch.full((n, cols), math.nan, device=DEV)
+    M.hpo_embedding(ids.to(DEV), torch.empty(0, cols, device=DEV), none)
+    assert not bool(none.any())
+
+
 # --------------------------------------------------------------------------
 # large tiles with ragged edges, and sums in parts of unequal lengths
 # --------------------------------------------------------------------------

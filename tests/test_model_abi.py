@@ -100,7 +100,8 @@ def test_embedding_grad_refusals(M, H):
     assert L.hpo_embedding_grad_workspace(5, 5, None) == H.HPO_EINVAL
     for n in (200, 8192, 8193, 65536, H.HPO_MUON_MAX_DIM):
         assert L.hpo_embedding_grad_workspace(n, 4096, ctypes.byref(out)) == H.HPO_OK
-        assert 8 * n <= out.value <= 16 * n + 2 * 4096 * 4 * (n // 16 + 1) + (n // 4096 + 1) * 8192 + 4096
+        # two lists of (row, token), two fp32 rows for each slab of 8 tokens at least, counts of blocks of 4096
+        assert 8 * n <= out.value <= 16 * n + 2 * 4096 * 4 * (n // 8 + 1) + (n // 4096 + 1) * 8192 + 4096
 
 
 def test_save_refusals(M, H):
