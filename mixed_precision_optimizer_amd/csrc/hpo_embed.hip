@@ -238,7 +238,6 @@ __global__ __launch_bounds__(kBucketThreads) void k_sort_bucket(EmbedGradArgs a,
 #pragma unroll
     for (int c = 0; c < kBucketHold; ++c)
         look(held[c]);
-#pragma unroll 4
     for (int c = kBucketHold; c < chunks; ++c) {
         const int t = first + 64 * c;
         look(t < n ? key_of(a, t) : none);
@@ -279,7 +278,6 @@ __global__ __launch_bounds__(kBucketThreads) void k_sort_bucket(EmbedGradArgs a,
 #pragma unroll
     for (int c = 0; c < kBucketHold; ++c)
         collect(first + 64 * c, held[c]);
-#pragma unroll 4
     for (int c = kBucketHold; c < chunks; ++c) {
         const int t = first + 64 * c;
         collect(t, t < n ? key_of(a, t) : none);

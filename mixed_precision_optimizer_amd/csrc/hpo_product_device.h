@@ -38,7 +38,10 @@ using Tile64 = Tile<2, 2, 1, 1>;
 
 constexpr int kRowBytes = 128;   /* of an operand row in a stage: 128 8-bit elements, or 64 16-bit ones */
 constexpr int kStepK = 64;        /* 16-bit elements of k in a stage */
-constexpr uint32_t kGroup = 8;        /* tile rows that neighbouring workgroups share */
+/* Tile rows that neighbouring workgroups share: 32 CUs of an XCD take 4 x 8 tiles of 256, and a gradient's row of A is
+ * twice as many bytes as its column of B (2, 4, 8, 16: G of 14336 x 4096 over 8192 tokens 896, 908, 925, 936 us, Y of
+ * 8192 x 14336 407, 400, 403, 414). */
+constexpr uint32_t kGroup = 4;
 
 /* Workgroups go to the 8 XCDs round-robin: each XCD gets one contiguous run of the work. */
 __device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n)
