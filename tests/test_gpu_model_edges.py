@@ -345,6 +345,31 @@ def test_embedding_grad_of_many_tokens(M, n, rows, cols, kind):
     assert torch.equal(su.bits(G)[~some], su.bits(grad)[~some])
 
 
+@pytest.mark.parametrize("n,rows,cols", [(2 ** 21, 2 ** 21, 3), (60000, 2 ** 21, 5), (128, 2 ** 21, 9), (200, 3, 2 ** 21)])
+def test_embedding_at_the_largest_sizes(M, n, rows, cols):
+    g = gen(n + cols)
+    ids = torch.randint(-2, rows + 2, (n,), generator=g)
+    ids[:2] = torch.tensor([rows - 1, 0])
+    dy = torch.randn(n, cols, generator=g).to(BF16)
+    grad = torch.randn(rows, cols, generator=g)
+    G = grad.to(DEV)
+    M.hpo_embedding_grad(ids.to(DEV), dy.to(DEV), G, workspace(M.hpo_embedding_grad_workspace(ids, grad)))
+    want, tol, some = mu.embedding_grad(ids, dy, grad, 1.0, 0)
+    mu.check(G, want, tol, f"{n} {rows} {cols}")
+    assert torch.equal(su.bits(G)[~some], su.bits(grad)[~some])
+    out = torch.empty(n, cols, device=DEV)
+    M.hpo_embedding(ids.to(DEV), grad.to(DEV), out)
+    assert torch.equal(out.cpu(), mu.embedding(ids, grad, 1.0, 0))
+
+
+@pytest.mark.parametrize("b,t,c,r", [(65535, 2, 33, 3), (1, 2 ** 21, 40, 4), (1, 2, 2 ** 21, 3), (1, 2, 2 ** 21 - 1, 3),
+                                     (1, 3, 40, 2 ** 21), (1, 3, 36, 2 ** 21 - 5)])
+def test_products_at_the_largest_sizes(M, b, t, c, r):
+    linear(M, b, t, c, r, BF16, "dense", dev=DEV)
+    dgrad(M, b, t, c, r, BF16, F32, "dense", dev=DEV)
+    wgrad(M, b, t, c, r, F16, F32, "dense", True, dev=DEV)
+
+
 # --------------------------------------------------------------------------
 # gradients against differences
 # --------------------------------------------------------------------------
