@@ -363,8 +363,8 @@ __global__ __launch_bounds__(T::kThreads) void k_mx8_linear(ProductArgs p)
  * A workgroup a CU takes tile after tile, and the stages of the next follow those of this one without a gap, so that
  * its first loads run beside this one's last products and results.
  *
- * 8192 x 4096 x 14336: 400 to 415 us from box to box, 2.32 to 2.40 PFLOP/s (side 128: 659 us); the matrix cores are busy half of the time at the
- * 2.0 GHz that the power leaves, and wavefronts wait for a fifth of it. */
+ * 8192 x 4096 x 14336: 400 to 415 us from box to box, 2.32 to 2.40 PFLOP/s (side 128: 659 us); the matrix
+ * cores are busy half of the time at the 2.0 GHz that the power leaves, and wavefronts wait for a fifth of it. */
 struct Big {
     static constexpr int kThreads = 256, kSide = 256;
 };

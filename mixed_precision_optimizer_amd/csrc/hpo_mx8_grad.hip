@@ -11,9 +11,10 @@
  * Bound by the matrix cores and the clock that the power leaves them (1.8 GHz, busy 56 % under counters), wavefronts
  * waiting for 30 % of the time.  dX of 8192 x 4096 from 14336 outputs takes 810 to 867 us from box to box (1.11 to
  * 1.19 PFLOP/s); G of 14336 x 4096 over 8192 tokens 908 to 961 (1.00 to 1.06; 3.5 rounds of tiles on 256 CUs in the
- * time of four); a bf16 product of the library alone, without the widening, takes 729 and 971 us.  Tiles of 256 by four wavefronts of 128 x 128, as in
- * hpo_mx8_linear, took 1568 and 1824 us: the widening is work for the vector units, and one wavefront a SIMD leaves
- * nobody to overlap it with.
+ * time of four); a bf16 product of the library alone, without the widening, takes 729 and 971 us.  Eight wavefronts share
+ * a tile of 256, so that the widening of one runs beside the products of another; four of 128 x 128 each, as in
+ * hpo_mx8_linear, took 1568 and 1824 us with loads that the compiler waits for (see load_lds16), when eight took 1028
+ * and 1178.
  */
 #include <hip/hip_runtime.h>
 
