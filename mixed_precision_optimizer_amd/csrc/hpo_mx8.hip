@@ -808,6 +808,13 @@ int64_t product_workspace(ProductKind kind, int64_t batch, int64_t m, int64_t n,
 
 hipError_t launch_product(ProductKind kind, ProductArgs p, hipStream_t stream)
 {
+    if (kind == kWgrad && p.k == 1) {
+        /* A lone row comes with stride 0, and with it every row of a stage would be this one: the rows behind the last
+         * token must lie behind the descriptors' ends.  (hpo_mx8_dgrad over one output has no rows in 16-byte pieces and
+         * goes through registers, which know where the rows end.) */
+        p.a_rs = (p.m + 7) / 8 * 8;
+        p.b_rs = (p.n + 15) / 16 * 16;
+    }
     Cut c = cut_of(kind, p.batch, p.m, p.n, p.k);
     if (c.tile == 256 && !is_big(kind, p, c.splits)) {
         c.tile = 128;
