@@ -28,3 +28,14 @@ def pieces(x, count):
         out.append((v, (e + 127).to(torch.uint8)))
         x = x - v * torch.exp2(e)
     return out, x
+
+
+def small_mx8(g, *shape):
+    """(e4m3 values, scale bytes) of two bits at scales that differ by up to four: multiples of 2^-3, at most 2."""
+    vals = torch.tensor([0.0, 1.0, -1.0, 1.5, -1.5, 2.0])
+    return (vals[torch.randint(0, 6, shape, generator=g)].to(E4M3),
+            torch.randint(125, 128, (*shape[:-1], -(-shape[-1] // 32)), generator=g).to(torch.uint8))
+
+
+def small_int(g, *shape):
+    return torch.randint(-3, 4, shape, generator=g)

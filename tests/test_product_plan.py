@@ -26,3 +26,23 @@ def test_parts_are_the_workspaces(kind):
         assert out.value == (4 * b * parts * m * n if parts > 1 else 0), (b, t, c, r)
         in_parts += parts > 1
     assert 300 < in_parts < 2700
+
+
+@pytest.mark.parametrize("drop", [0, 3, 195, 390])
+def test_a_lost_stage_shows_in_an_exact_case(drop):
+    """Of the deepest exact case (k = 50000, results in fp16) one stage of 128 left out, or at half its scale, changes
+    most results; of a gradient's (k = 30000, fp32) one of 64 changes nearly all."""
+    import torch
+
+    import model_util as mu
+    import product_sums as ps
+    g = torch.Generator().manual_seed(drop)
+    a, b = (mu.mx_values(*ps.small_mx8(g, 50, 50000)) for _ in range(2))
+    at = slice(128 * drop, min(128 * drop + 128, 50000))
+    whole, lost = a @ b.T, a[:, at] @ b[:, at].T
+    for other in (whole - lost, whole - lost / 2):
+        assert float((whole.half() != other.half()).double().mean()) > 0.75
+    a = ps.small_int(g, 50, 30000).double()
+    lost = a[:, 64 * drop: 64 * drop + 64] @ b[:, 64 * drop: 64 * drop + 64].T
+    whole = a @ b[:, :30000].T
+    assert float((whole.float() != (whole - lost).float()).double().mean()) > 0.95
