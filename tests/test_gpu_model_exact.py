@@ -16,9 +16,9 @@ from test_gpu_model import BF16, DEV, F16, F32, Guarded, M, blank, gen, linear_e
 pytestmark = pytest.mark.gpu
 
 
-def aligned(layout, *cols):
-    """Whether rows of so many elements are whole 16-byte pieces apart in this layout."""
-    return layout == "aligned" or (layout in ("dense", "rows") and all(c % 16 == 0 for c in cols))
+def aligned(layout, *row_bytes):
+    """Whether rows of so many bytes are whole 16-byte pieces apart in this layout."""
+    return layout == "aligned" or (layout in ("dense", "rows") and all(n % 16 == 0 for n in row_bytes))
 
 
 def check_exact(got, want, tag):
@@ -86,3 +86,32 @@ def test_wgrad_in_parts(M, shape, side, parts, layout):
     assert pp.plan("wgrad", *shape, layout == "aligned")[:2] == (side if layout == "aligned" else min(side, 128), parts)
     wgrad_exact(M, *shape, BF16, F32, layout, True)
     wgrad_exact(M, *shape, F16, BF16, layout, False)
+
+
+# --------------------------------------------------------------------------
+# stacks on large tiles
+# --------------------------------------------------------------------------
+# A workgroup of the forward tiles of 256 takes tile after tile: more of them than 256 workgroups, over the borders of
+# matrices, ragged on both sides, whole sums and parts
+LINEAR_STACKS = [((2, 2304, 512, 2304), 162, 1), ((4, 2300, 528, 2600), 396, 1), ((5, 2100, 1040, 2300), 405, 1),
+                 ((2, 1010, 50000, 1000), 32, 8)]
+GRAD_STACKS = [("dgrad", (3, 1500, 2000, 1000), 144, 1), ("dgrad", (5, 2100, 2000, 1000), 360, 1),
+               ("dgrad", (4, 250, 704, 16000), 12, 16), ("wgrad", (3, 250, 512, 16000), 378, 1),
+               ("wgrad", (2, 501, 6000, 1000), 192, 1), ("wgrad", (2, 20000, 704, 504), 12, 16)]
+
+
+@pytest.mark.parametrize("shape,tiles,parts", LINEAR_STACKS)
+@pytest.mark.parametrize("layout", ["dense", "aligned", "rows"])
+def test_linear_stacks_of_large_tiles(M, shape, tiles, parts, layout):
+    assert aligned(layout, shape[2]) and pp.plan("linear", *shape) == (256, parts, tiles)
+    linear_exact(M, *shape, BF16 if parts == 1 else F16, layout, dev=DEV)
+
+
+@pytest.mark.parametrize("kind,shape,tiles,parts", GRAD_STACKS)
+@pytest.mark.parametrize("layout", ["dense", "aligned", "rows"])
+def test_gradient_stacks_of_large_tiles(M, kind, shape, tiles, parts, layout):
+    assert aligned(layout, shape[2], 2 * shape[3]) and pp.plan(kind, *shape) == (256, parts, tiles)
+    if kind == "dgrad":
+        dgrad_exact(M, *shape, BF16, F32, layout)
+    else:
+        wgrad_exact(M, *shape, BF16, F32, layout, True)
