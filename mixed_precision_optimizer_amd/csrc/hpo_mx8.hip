@@ -823,14 +823,17 @@ hipError_t launch_product(ProductKind kind, ProductArgs p, hipStream_t stream)
     }
     const bool direct = is_direct(kind, p, c.tile);
     const int64_t grid = p.batch * c.tiles_m * c.tiles_n * c.splits;
-    if (grid > INT32_MAX)
+    /* work_of counts to INT32_MAX, a launch's threads to UINT32_MAX; the forward tiles of 256 are items of 256 workgroups */
+    const bool items = kind == kLinear && c.tile == 256;
+    const int64_t threads = c.tile == 256 ? Tile256::kThreads : Tile128::kThreads;
+    if (grid > INT32_MAX || (!items && grid * threads > UINT32_MAX))
         return hipErrorInvalidConfiguration;
     p.tiles_m = static_cast<int32_t>(c.tiles_m);
     p.tiles_n = static_cast<int32_t>(c.tiles_n);
     p.splits = c.splits;
     const uint32_t g = static_cast<uint32_t>(grid);
     hipError_t e = kind != kLinear ? launch_mx8_grad(kind == kWgrad, p, c.tile, direct, g, stream)
-                   : c.tile == 256 ? launch(k_mx8_linear_big, dim3(std::min<uint32_t>(g, 256)), Big::kThreads, stream, p, g)
+                   : items         ? launch(k_mx8_linear_big, dim3(std::min<uint32_t>(g, 256)), Big::kThreads, stream, p, g)
                    : c.tile == 128 ? linear_tile<Tile128>(p, direct, g, stream)
                                    : linear_tile<Tile64>(p, direct, g, stream);
     if (e != hipSuccess || p.splits == 1)

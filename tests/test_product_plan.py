@@ -46,3 +46,23 @@ def test_a_lost_stage_shows_in_an_exact_case(drop):
     lost = a[:, 64 * drop: 64 * drop + 64] @ b[:, 64 * drop: 64 * drop + 64].T
     whole = a @ b[:, :30000].T
     assert float((whole.float() != (whole - lost).float()).double().mean()) > 0.95
+
+
+@pytest.mark.parametrize("kind,shape", [("dgrad", (1024, 1, 1 << 20, 8)), ("wgrad", (32768, 8, 32768, 64)),
+                                        ("linear", (1, 1 << 20, 16, 1 << 19))])
+def test_more_threads_than_a_launch_holds_are_refused(kind, shape):
+    """2^24 tiles of 256 threads and more: a launch has 2^32 - 1 at most.  The refusal is the call's own, found before
+    anything is enqueued: a launch that the runtime refuses would leave its error to the caller's next check."""
+    from mixed_precision_optimizer_amd import hpo, hpo_model as M
+    b, t, c, r = shape
+    lib, at, size = M.load(), 0x10000, 1 << 60
+    side, parts, tiles = pp.plan(kind, *shape)
+    assert side < 256 and tiles * parts * 256 >= 2 ** 32
+
+    def stack(rows, cols, dtype):
+        return ctypes.byref(M.c_stack(at, b, rows, cols, rows * cols, cols, dtype, 0))
+    x, w, dy = stack(t, c, 16), stack(r, c, 16), stack(t, r, 0)
+    st = {"linear": lambda: lib.hpo_mx8_linear(x, at, w, at, dy, at, size, None),
+          "dgrad": lambda: lib.hpo_mx8_dgrad(dy, w, at, stack(t, c, 0), at, size, None),
+          "wgrad": lambda: lib.hpo_mx8_wgrad(dy, x, at, 1.0, 1, stack(r, c, 1), at, size, None)}[kind]()
+    assert st == hpo.HPO_EINVAL and "more tiles" in hpo.hpo_last_error(), (st, hpo.hpo_last_error())
