@@ -4,8 +4,8 @@
  * (hpo_embedding_grad).
  *
  * Both are bound by HBM.  The lookup moves one table row and one output row per token; a group of
- * lanes takes a row, eight elements a lane: 8192 tokens of 4096 bf16 take 24 us, 19 of them in the kernel (the rows of
- * repeated tokens come from L2).
+ * lanes takes a row, eight elements a lane: 8192 tokens of 4096 bf16 take 24 to 26 us, 19 where table and results stay in
+ * the 256 MB cache from call to call (the rows of repeated tokens come from L2).
  *
  * The gradient adds rows of dY that belong to one token.  Atomics on the main grad would leave
  * the order of the sums to chance and pass over G once per token, so the tokens are sorted
@@ -14,8 +14,9 @@
  * token comes.  A run of equal tokens inside a slab goes straight into its row of G, each row read and
  * written once; a run that crosses a slab's border leaves its parts in the workspace, and a last
  * launch adds these in order.  Up to 128 tokens one launch does without the sort: the first
- * token of its kind adds up the others.  8192 tokens of 4096 into an fp32 main grad take 69 us: sort 12, sums 35 (5.7
- * TB/s), join 5, and the starts of three launches.
+ * token of its kind adds up the others.  8192 tokens of 4096 into an fp32 main grad take 69 to 71 us: sort 13, sums 53 (196 MB
+ * from and to HBM at 3.7 TB/s), join 6, no gaps between the launches; 51 us, 34 of them the sums, where one call's
+ * operands are in the 256 MB cache from the call before.
  */
 #include <hip/hip_runtime.h>
 
@@ -203,7 +204,13 @@ __device__ __forceinline__ int32_t key_of(const EmbedGradArgs& a, int64_t t)
     return static_cast<int32_t>(row < 0 ? a.rows : row);
 }
 
-/* One launch for up to kBucketMax tokens: workgroup b looks through all of them for the rows with row mod
+/* One launch for up to kBucketMax tokens, as every workgroup looks through all of them; counting passes (two or four
+ * launches) behind that.  Whole calls, in microseconds, by buckets and by counting: 4096 tokens of 1024 into 32000 rows 22
+ * and 34, 16384 43 and 54, 32768 65 and 65, 65536 108 and 84, 131072 227 and 153; into 1000 rows 16384 39 and 40, 32768 57
+ * and 47; of 64 into 128256 rows 32768 39 and 46, 65536 68 and 53.  So the two meet between 16384 and 65536 tokens, and up
+ * to the limit the worst is 1.6 times the better.
+ *
+ * Workgroup b looks through all of them for the rows with row mod
  * gridDim.x = b, which are its part of the list (behind those of the buckets before it), collects them in
  * order of position, and sorts them by the rest of the row.  So equal rows come together, though not in
  * their order; ids without a row come last. */
@@ -651,7 +658,11 @@ __global__ __launch_bounds__(64 * kJoinWaves) void k_grad_join(EmbedGradArgs a, 
     }
 }
 
-constexpr int kFewMax = 128;   /* tokens up to which no sort is needed */
+/* Tokens up to which no sort is needed: every token looks through all of them.  Without a sort and with it, in
+ * microseconds, rows of 4096 elements into 32000 rows, tokens as in text: 16 tokens 4 and 15, 64 8 and 15, 128 14 and 17, 192
+ * 21 and 17; rows of 64 elements (eight lanes each): 64 11 and 15, 128 24 and 17.  One token all along is one lane group's
+ * work without the sort: 16 7 and 15, 64 20 and 16, 128 39 and 16. */
+constexpr int kFewMax = 128;
 
 /* LANES lanes take a token's row: the first token of its kind adds up all of them. */
 template <int YT, int GT, int LANES>
@@ -737,8 +748,8 @@ hipError_t embedding_out(const EmbedArgs& a, hipStream_t stream)
 }
 
 /* Tokens of a slab: the more the fewer runs cross borders, as long as there are some 6144 wavefronts (6 a
- * SIMD).  The sums and the join of bf16 rows: 20000 of 1001 take 27 us with slabs of 8 and 34 with 16; 8192 of 4096
- * 44 and 39. */
+ * SIMD).  The sums and the join of bf16 rows, with operands in the 256 MB cache: 20000 of 1001 take 27 us with slabs of
+ * 8 and 34 with 16; 8192 of 4096 44 and 39. */
 int32_t slab_length(int64_t n, int64_t cols)
 {
     const int64_t pieces = (cols + 511) / 512;

@@ -8,13 +8,14 @@
  * contiguous: the fragments come from LDS by transposing reads, for wgrad dY's as well.  The scale blocks lie along
  * the other side, so no scale could stay outside of the sum.
  *
- * Bound by the matrix cores and the clock that the power leaves them (1.8 GHz, busy 56 % under counters), wavefronts
- * waiting for 30 % of the time.  dX of 8192 x 4096 from 14336 outputs takes 810 to 867 us from box to box (1.11 to
- * 1.19 PFLOP/s); G of 14336 x 4096 over 8192 tokens 908 to 961 (1.00 to 1.06; 3.5 rounds of tiles on 256 CUs in the
- * time of four); a bf16 product of the library alone, without the widening, takes 729 and 971 us.  Eight wavefronts share
- * a tile of 256, so that the widening of one runs beside the products of another; four of 128 x 128 each, as in
- * hpo_mx8_linear, took 1568 and 1824 us with loads that the compiler waits for (see load_lds16), when eight took 1028
- * and 1178.
+ * Bound by the matrix cores (busy 55 % of dX's time, 46 % of G's) and the clock that the power leaves them (1.7 to 2.2
+ * GHz under counters), wavefronts waiting for a third of the time.  dX of 8192 x 4096 from 14336 outputs takes 810 to
+ * 867 us from box to box (1.11 to 1.19 PFLOP/s); G of 14336 x 4096 over 8192 tokens 908 to 961 (1.00 to 1.06; 3.5 rounds of
+ * tiles on 256 CUs in the time of four); call after call 834 and 936, in the first ten on a card that was idle 920 to 1150 and
+ * 1060 to 1330, while its clock swings.  A bf16 product of the library alone, without the widening, takes 729 and 971 us.
+ * Eight wavefronts share a tile of 256, so that the widening of one runs beside the products of another; four of 128 x 128
+ * each, as in hpo_mx8_linear, took 1568 and 1824 us with loads that the compiler waits for (see load_lds16), when eight took
+ * 1028 and 1178.
  */
 #include <hip/hip_runtime.h>
 
