@@ -80,8 +80,8 @@ hpo_status hpo_mx8_save(const hpo_stack* x, const hpo_stack* q, uint8_t* d_scale
  * all that follows, are rounded to fp32.  In the root mean square that loses 1.5e-5 of Y where x and w are normal, 3e-5 to
  * 4e-5 where x's channels differ in size by a factor of e (their logarithms' deviation): a hundredth and a fortieth of the
  * rounding to bf16 (1.7e-3), a fourteenth and a sixth of that to fp16 (2.1e-4), and the reason why Y is not fp32.
- * dgrad and wgrad take X^ and W^ in dY's type: exact in bf16 (values below 2^-126 lose bits) and, with fp16, rounded to
- * it: exact for values that were fp16 before hpo_mx8_save, infinite above 65504.  wgrad rounds the product with scale
+ * dgrad and wgrad take X^ and W^ in dY's type: exact in bf16 (below 2^-126 rounded to its subnormals) and, with fp16,
+ * rounded to it: exact for values that were fp16 before hpo_mx8_save, infinite above 65504.  wgrad rounds the product with scale
  * and the sum with G to fp32, then once to G's type; with accumulate = 0 G is not read.
  * A block of NaN makes NaN of every result that it enters.  No tokens or no inner
  * elements: sums of nothing, so Y and dX are zeros, and G is kept or zeros.
